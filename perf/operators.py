@@ -107,10 +107,12 @@ def _lengths(total, batch, gen):
 
 
 def _quantise(x):
-    """Rows of 8-bit values and their scales."""
+    """Rows of 8-bit values and their scales.  (Tensor by tensor: with a plain number torch multiplies by a rounded
+    reciprocal instead of dividing.)"""
     x = x.float()
     a = x.abs().amax(-1, keepdim=True).clamp(min=2.0 ** -110)
-    return (x * (448.0 / a)).to(F8), (a / 448.0).squeeze(-1)
+    top = torch.full_like(a, 448.0)
+    return (x * (top / a)).to(F8), (a / top).squeeze(-1)
 
 
 def _pool(case, lens, gen, cpu, poison, most=0):
