@@ -356,6 +356,122 @@ int infllm2_decode_step(const infllm2_decode_state* st, const void* q, const voi
                         void* out, void* workspace, size_t workspace_bytes, const infllm2_params* p,
                         void* stream);
 
+/* ---------------------------------------------------------------------
+ * Rotary positions of the queries and keys of a packed batch (the step
+ * before infllm2_compress_k, infllm2_dense_attn and a cache write), with one
+ * to four position axes (time, height, width, ...).  For token t, head h and
+ * pair i < rot / 2 of axis a(i), with theta = pos[a(i), t] * freq_i:
+ *   y1 = x1 cos(theta) - x2 sin(theta),  y2 = x2 cos(theta) + x1 sin(theta)
+ * where (x1, x2) are elements (i, i + rot/2), or (2i, 2i + 1) when
+ * interleaved; elements from rot on are copied.  The first sections[0] pairs
+ * belong to axis 0, the next sections[1] to axis 1, and so on.
+ * infllm2_rope_backward takes the gradients of the outputs and returns those
+ * of the inputs (the rotation by -theta).  Arithmetic is fp32, rounded once to
+ * the tensors' type.  An angle is formed modulo one turn in 64-bit fixed
+ * point, so it is exact to 2^-32 of a turn at any int32 position (negative ones
+ * included).
+ *
+ * infllm2_rope_init fills a spec on the host: freq_i = base^(-2i/rot), or
+ * inv_freq[i] (host array of rot/2 doubles, any scaled frequencies; base is
+ * then ignored).  rot is even, at most 128; sections must sum to rot/2 (it may
+ * be NULL for one axis).  The spec is plain data and may be copied.
+ *   q    [total, h_q, d], k [total, h_kv, d]: bf16 (INFLLM2_OUT_BF16) or fp32
+ *        (INFLLM2_OUT_F32), both of dtype; d is 64 or 128, rot <= d
+ *   pos  int32 [n_axes, total] on the device
+ *   q_out, k_out  as q and k; may be q and k themselves (in place), and must
+ *        not overlap them otherwise
+ * total * (h_q + h_kv) above 2^31 - 1 is INFLLM2_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------- */
+#define INFLLM2_ROPE_MAX_AXES 4
+#define INFLLM2_ROPE_MAX_PAIRS 64
+typedef struct {
+  int32_t rot;
+  int32_t n_axes;
+  int32_t sections[INFLLM2_ROPE_MAX_AXES];
+  int32_t interleaved;
+  int32_t reserved;
+  uint64_t turns[INFLLM2_ROPE_MAX_PAIRS];   /* frac(freq_i / 2 pi) * 2^64 */
+} infllm2_rope_spec;
+
+int infllm2_rope_init(infllm2_rope_spec* r, int32_t rot, int32_t n_axes, const int32_t* sections,
+                      int32_t interleaved, double base, const double* inv_freq);
+int infllm2_rope(const void* q, const void* k, int32_t dtype, const int32_t* pos, int64_t total, int32_t h_q,
+                 int32_t h_kv, int32_t d, const infllm2_rope_spec* r, void* q_out, void* k_out, void* stream);
+int infllm2_rope_backward(const void* dq_rot, const void* dk_rot, int32_t dtype, const int32_t* pos, int64_t total,
+                          int32_t h_q, int32_t h_kv, int32_t d, const infllm2_rope_spec* r, void* dq, void* dk,
+                          void* stream);
+
+/* ---------------------------------------------------------------------
+ * Paged key-value cache.  The caller owns a pool of pages and a table:
+ *   k_pages, v_pages  [n_pages, h_kv, page_size, d], bf16 (INFLLM2_KV_BF16) or
+ *                     e4m3 (INFLLM2_KV_E4M3)
+ *   k_scale, v_scale  fp32 [n_pages, h_kv, page_size] (e4m3 only; else ignored)
+ *   block_table       int32 [batch, max_pages] on the device: position u of
+ *                     sequence b is slot u % page_size of page
+ *                     block_table[b, u / page_size].  Sequences may share pages.
+ * page_size is a power of two from 16 to 1024, d is 64 or 128.  An int32
+ * array needs 4-byte alignment, every other pointer 16-byte alignment.  Only
+ * the table entries of positions that a call touches are read; an entry
+ * outside [0, n_pages) or a position past max_pages * page_size - 1 is skipped
+ * and recorded in the device status word as INFLLM2_ERR_DEVICE_BOUNDS.
+ *
+ * infllm2_paged_write puts K and V rows ([total, h_kv, d] bf16) into their
+ * pages: row i of sequence b (packed row cu_seqlens[b] + i) goes to position
+ * start[b] + i.  With cu_seqlens NULL there is one row a sequence (total ==
+ * batch).  A sequence with a negative start is left out, and so are packed rows
+ * behind cu_seqlens[batch].  Two rows of one call must not go to the same slot.
+ * 8 bits: with a = max(max |x|, 2^-110) over the d values of a row, scale = a / 448 and
+ * y = e4m3(x * (448 / a)), fp32 operations rounded to nearest; a row that
+ * holds an infinity or NaN reads back as NaN.
+ *
+ * infllm2_paged_read brings positions 0 .. len-1 of every sequence back into
+ * packed rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of K and V ([total, h_kv, d]
+ * bf16): bf16(y * scale), or the bf16 row.  Rows behind cu_seqlens[batch], and
+ * rows whose page is out of range, are left as they were.
+ * ------------------------------------------------------------------- */
+enum { INFLLM2_KV_BF16 = 0, INFLLM2_KV_E4M3 = 1 };
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t h_kv;
+  int32_t d;
+  int32_t dtype;
+} infllm2_paged_cache;
+
+int infllm2_paged_write(const infllm2_paged_cache* c, const void* K, const void* V, const int32_t* start,
+                        const int32_t* cu_seqlens, int64_t total, void* stream);
+int infllm2_paged_read(const infllm2_paged_cache* c, void* K, void* V, const int32_t* cu_seqlens, int64_t total,
+                       void* stream);
+
+/* Attention of one new token a sequence over its whole paged cache, the dense
+ * side of the dense/sparse switch at decode (a sequence past dense_threshold
+ * goes to infllm2_decode_step).  For query head h of group g and n = seq_len[b]
+ * (device, int32 [batch]; the new token's own row already written):
+ *   out[b,h] = sum_{u<n} softmax_u(scale * q[b,h] . K[u,g]) V[u,g]
+ *   lse[b,h] = log2 sum_{u<n} 2^(scale * log2(e) * q[b,h] . K[u,g])
+ *   q    bf16 [batch, h_q, d];  out [batch, h_q, d] bf16 or fp32 (out_dtype)
+ *   lse  fp32 [batch, h_q], or NULL
+ * A sequence of length 0, or whose every score is -infinity, gives zeros and
+ * -infinity.  Slots at or past seq_len[b] are not read.  A length outside
+ * [0, max_pages * page_size] is recorded as INFLLM2_ERR_DEVICE_BOUNDS and
+ * counts as 0; rows of a page out of range count as zeros.
+ * Of p, scale is used.  workspace: at least infllm2_paged_workspace_bytes bytes
+ * (device, on the current device; contents need no initialisation and carry
+ * nothing between calls; one workspace must not serve two calls in flight at
+ * once).  The result does not depend on scheduling.  Two launches, no host
+ * synchronisation, graph-capturable; lengths may change between replays. */
+size_t infllm2_paged_workspace_bytes(const infllm2_paged_cache* c, int32_t h_q);
+int infllm2_paged_decode_attn(const infllm2_paged_cache* c, const void* q, int32_t h_q, const int32_t* seq_len,
+                              void* out, int32_t out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                              const infllm2_params* p, void* stream);
+
 /* Device status word (per device).  Returns INFLLM2_OK or the first
  * INFLLM2_ERR_DEVICE_* recorded by a kernel since the last clear.
  * Synchronises the device. */

@@ -27,12 +27,17 @@ __all__ = [
     "infllm2_probe_l2_gather",
     "DecodeState", "make_decode_state", "infllm2_decode_workspace_bytes", "infllm2_decode_build_caches",
     "infllm2_decode_step", "OUT_BF16", "OUT_F32", "LSE_APPROX", "LSE_EXACT",
+    "RopeSpec", "make_rope", "infllm2_rope", "infllm2_rope_backward",
+    "PagedCache", "make_paged_cache", "infllm2_paged_write", "infllm2_paged_read", "infllm2_paged_workspace_bytes",
+    "infllm2_paged_decode_attn", "KV_BF16", "KV_E4M3",
 ]
 
 LSE_APPROX = 0
 LSE_EXACT = 1
 OUT_BF16 = 0
 OUT_F32 = 1
+KV_BF16 = 0
+KV_E4M3 = 1
 
 
 class InfLLM2Error(RuntimeError):
@@ -65,6 +70,22 @@ class DecodeState(ctypes.Structure):
         ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("k_c1", ctypes.c_void_p),
         ("k_c2", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("batch", ctypes.c_int32),
         ("capacity", ctypes.c_int32), ("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+    ]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [
+        ("rot", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+        ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64),
+    ]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
     ]
 
 
@@ -112,6 +133,16 @@ def lib() -> ctypes.CDLL:
         "infllm2_decode_build_caches": (ctypes.c_int, [ctypes.POINTER(DecodeState), pp, _P]),
         "infllm2_decode_step": (ctypes.c_int, [ctypes.POINTER(DecodeState), _P, _P, _P, _P, _P, ctypes.c_size_t, pp,
                                                 _P]),
+        "infllm2_rope_init": (ctypes.c_int, [ctypes.POINTER(RopeSpec), i32, i32, ctypes.POINTER(i32), i32,
+                                             ctypes.c_double, ctypes.POINTER(ctypes.c_double)]),
+        "infllm2_rope": (ctypes.c_int, [_P, _P, i32, _P, i64, i32, i32, i32, ctypes.POINTER(RopeSpec), _P, _P, _P]),
+        "infllm2_rope_backward": (ctypes.c_int, [_P, _P, i32, _P, i64, i32, i32, i32, ctypes.POINTER(RopeSpec), _P,
+                                                 _P, _P]),
+        "infllm2_paged_write": (ctypes.c_int, [ctypes.POINTER(PagedCache), _P, _P, _P, _P, i64, _P]),
+        "infllm2_paged_read": (ctypes.c_int, [ctypes.POINTER(PagedCache), _P, _P, _P, i64, _P]),
+        "infllm2_paged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PagedCache), i32]),
+        "infllm2_paged_decode_attn": (ctypes.c_int, [ctypes.POINTER(PagedCache), _P, i32, _P, _P, i32, _P, _P,
+                                                     ctypes.c_size_t, pp, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -346,3 +377,152 @@ def infllm2_decode_step(st: DecodeState, q: torch.Tensor, k_new: torch.Tensor, v
     rc = lib().infllm2_decode_step(ctypes.byref(st), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out), _ptr(workspace),
                                    ws_bytes, ctypes.byref(params or default_params()), _stream(stream))
     _check("infllm2_decode_step", rc)
+
+
+# ------------------------------------------------------------------ rotary positions, paged cache
+def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """The data pointer of a contiguous tensor of this dtype and shape on `device`; raises otherwise."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise InfLLM2Error(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                           f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class _on:
+    """The CUDA device of `t` as the current one for a call: a launch goes to the current device.  The library has no
+    CPU path, so a tensor elsewhere is refused."""
+
+    def __init__(self, t: torch.Tensor):
+        if t.device.type != "cuda":
+            raise InfLLM2Error(f"expected CUDA tensors, got one on {t.device}")
+        self.to, self.back = t.device.index, torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.to != self.back:
+            torch.cuda.set_device(self.to)
+
+    def __exit__(self, *exc):
+        if self.to != self.back:
+            torch.cuda.set_device(self.back)
+
+
+def make_rope(rot: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None, interleaved: bool = False,
+              inv_freq: Optional[Sequence[float]] = None) -> RopeSpec:
+    """Rotary positions over the first `rot` elements of a head.  `sections`: pairs of each position axis (one axis by
+    default); `inv_freq`: rot/2 frequencies in place of base^(-2i/rot).  Host values only; the spec may be kept."""
+    r = RopeSpec()
+    sec = [rot // 2] if sections is None else [int(x) for x in sections]
+    freq = None
+    if inv_freq is not None:
+        freq = [float(x) for x in inv_freq]
+        if len(freq) != rot // 2:
+            raise InfLLM2Error(f"inv_freq has {len(freq)} frequencies, rot / 2 is {rot // 2}")
+        freq = (ctypes.c_double * len(freq))(*freq)
+    rc = lib().infllm2_rope_init(ctypes.byref(r), rot, len(sec), (ctypes.c_int32 * len(sec))(*sec), int(interleaved),
+                                 base, freq)
+    _check("infllm2_rope_init", rc)
+    return r
+
+
+def _rope(name: str, q, k, pos, rope, q_out, k_out, stream) -> None:
+    with _on(q):
+        if q.dim() != 3 or k.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float32):
+            raise InfLLM2Error(f"{name}: q and k are [total, heads, d] tensors of bf16 or fp32")
+        (total, h_q, d), h_kv, dt, dev = q.shape, k.shape[1], q.dtype, q.device
+        od = OUT_F32 if dt == torch.float32 else OUT_BF16
+        if pos.dim() == 1:
+            pos = pos[None]
+        rc = getattr(lib(), name)(_expect("q", q, dt, (total, h_q, d), dev), _expect("k", k, dt, (total, h_kv, d), dev),
+                                  od, _expect("pos", pos, torch.int32, (rope.n_axes, total), dev), total, h_q, h_kv, d,
+                                  ctypes.byref(rope), _expect("q_out", q_out, dt, q.shape, dev),
+                                  _expect("k_out", k_out, dt, k.shape, dev), _stream(stream))
+    _check(name, rc)
+
+
+def infllm2_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, rope: RopeSpec, q_out: torch.Tensor,
+                 k_out: torch.Tensor, stream=None) -> None:
+    """Rotates q [total, h_q, d] and k [total, h_kv, d] (bf16 or fp32) to their positions, int32 [axes, total] (or
+    [total] for one axis).  q_out and k_out may be q and k."""
+    _rope("infllm2_rope", q, k, pos, rope, q_out, k_out, stream)
+
+
+def infllm2_rope_backward(dq_rot: torch.Tensor, dk_rot: torch.Tensor, pos: torch.Tensor, rope: RopeSpec,
+                          dq: torch.Tensor, dk: torch.Tensor, stream=None) -> None:
+    """Gradients of infllm2_rope's inputs from those of its outputs (bf16 or fp32, such as the fp32 dQ and dK of
+    infllm2_sparse_attn_backward); may be in place."""
+    _rope("infllm2_rope_backward", dq_rot, dk_rot, pos, rope, dq, dk, stream)
+
+
+def make_paged_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                     k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None) -> PagedCache:
+    """Paged cache over caller-owned device tensors: pages [n_pages, h_kv, page_size, d], bf16 or float8_e4m3fn (then
+    with fp32 scales [n_pages, h_kv, page_size]), block_table int32 [batch, max_pages].  Keeps references."""
+    dev, dt, f8 = k_pages.device, k_pages.dtype, k_pages.dtype == torch.float8_e4m3fn
+    if k_pages.dim() != 4 or not (f8 or dt == torch.bfloat16) or block_table.dim() != 2:
+        raise InfLLM2Error("pages are [n_pages, h_kv, page_size, d] tensors of bf16 or float8_e4m3fn, the table is "
+                           "[batch, max_pages]")
+    if f8 != (k_scale is not None) or f8 != (v_scale is not None):
+        raise InfLLM2Error("scales go with float8_e4m3fn pages, and only with them")
+    c = PagedCache()
+    c.k_pages, c.v_pages = (_expect(n, t, dt, k_pages.shape, dev) for n, t in (("k_pages", k_pages),
+                                                                               ("v_pages", v_pages)))
+    if f8:
+        c.k_scale = _expect("k_scale", k_scale, torch.float32, k_pages.shape[:3], dev)
+        c.v_scale = _expect("v_scale", v_scale, torch.float32, k_pages.shape[:3], dev)
+    c.block_table = _expect("block_table", block_table, torch.int32, block_table.shape, dev)
+    c.n_pages, c.h_kv, c.page_size, c.d = k_pages.shape
+    c.batch, c.max_pages = block_table.shape
+    c.dtype = KV_E4M3 if f8 else KV_BF16
+    c._keep = (k_pages, v_pages, block_table, k_scale, v_scale)  # noqa: SLF001
+    return c
+
+
+def infllm2_paged_write(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, start: torch.Tensor,
+                        cu_seqlens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Writes packed rows K, V [total, h_kv, d] (bf16) into the pages: row i of sequence b goes to position
+    start[b] + i.  cu_seqlens int32 [batch + 1]; None: one row a sequence."""
+    with _on(K):
+        shape, dev = (K.shape[0], cache.h_kv, cache.d), cache._keep[0].device  # noqa: SLF001
+        rc = lib().infllm2_paged_write(
+            ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev), _expect("V", V, torch.bfloat16, shape, dev),
+            _expect("start", start, torch.int32, (cache.batch,), dev),
+            None if cu_seqlens is None else _expect("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), dev),
+            K.shape[0], _stream(stream))
+    _check("infllm2_paged_write", rc)
+
+
+def infllm2_paged_read(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, cu_seqlens: torch.Tensor,
+                       stream=None) -> None:
+    """Reads positions 0 .. len-1 of every sequence into the packed rows of K, V [total, h_kv, d] (bf16)."""
+    with _on(K):
+        shape, dev = (K.shape[0], cache.h_kv, cache.d), cache._keep[0].device  # noqa: SLF001
+        rc = lib().infllm2_paged_read(
+            ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev), _expect("V", V, torch.bfloat16, shape, dev),
+            _expect("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), dev), K.shape[0], _stream(stream))
+    _check("infllm2_paged_read", rc)
+
+
+def infllm2_paged_workspace_bytes(cache: PagedCache, h_q: int) -> int:
+    with _on(cache._keep[0]):  # noqa: SLF001
+        return int(lib().infllm2_paged_workspace_bytes(ctypes.byref(cache), h_q))
+
+
+def infllm2_paged_decode_attn(cache: PagedCache, q: torch.Tensor, seq_len: torch.Tensor, out: torch.Tensor,
+                              workspace: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                              params: Optional[Params] = None, stream=None) -> None:
+    """Attention of one token a sequence, q [batch, h_q, d] (bf16), over the first seq_len[b] positions of its pages
+    (its own row among them) into out [batch, h_q, d] (bf16 or fp32) and, if given, lse fp32 [batch, h_q]."""
+    with _on(q):
+        dev, batch = cache._keep[0].device, cache.batch  # noqa: SLF001
+        if q.dim() != 3 or out.dtype not in (torch.bfloat16, torch.float32):
+            raise InfLLM2Error("q is [batch, h_q, d], out bf16 or fp32")
+        h_q = q.shape[1]
+        shape = (batch, h_q, cache.d)
+        rc = lib().infllm2_paged_decode_attn(
+            ctypes.byref(cache), _expect("q", q, torch.bfloat16, shape, dev), h_q,
+            _expect("seq_len", seq_len, torch.int32, (batch,), dev), _expect("out", out, out.dtype, shape, dev),
+            OUT_F32 if out.dtype == torch.float32 else OUT_BF16,
+            None if lse is None else _expect("lse", lse, torch.float32, (batch, h_q), dev),
+            _expect("workspace", workspace, workspace.dtype, workspace.shape, dev),
+            workspace.numel() * workspace.element_size(), ctypes.byref(params or default_params()), _stream(stream))
+    _check("infllm2_paged_decode_attn", rc)

@@ -28,6 +28,9 @@
 #include "pair_attn.cu"
 #include "decode.cu"
 #include "backward.cu"
+#include "rope.cu"
+#include "paged_cache.cu"
+#include "paged_attn.cu"
 #include "probe.cu"
 #include "../../include/infllm2_measure.h"
 
@@ -387,6 +390,165 @@ int infllm2_decode_step(const infllm2_decode_state* st, const void* q, const voi
   if (workspace_bytes < P.bytes) return INFLLM2_ERR_WORKSPACE_TOO_SMALL;
   cudaError_t e = launch_decode_step(st, q, k_new, v_new, out, workspace, P, p->n_init, p->n_local, p->top_k,
                                      softmax_scale(p, st->d), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INFLLM2_OK : cuda_fail(e);
+}
+
+int infllm2_rope_init(infllm2_rope_spec* r, int32_t rot, int32_t n_axes, const int32_t* sections, int32_t interleaved,
+                      double base, const double* inv_freq) {
+  if (!r || rot < 2 || (rot & 1) || n_axes < 1 || (n_axes > 1 && !sections)) return INFLLM2_ERR_INVALID_ARG;
+  if (rot / 2 > INFLLM2_ROPE_MAX_PAIRS || n_axes > INFLLM2_ROPE_MAX_AXES) return INFLLM2_ERR_UNSUPPORTED;
+  if (!inv_freq && !(base > 0. && base < INFINITY)) return INFLLM2_ERR_INVALID_ARG;
+  infllm2_rope_spec s;
+  memset(&s, 0, sizeof(s));
+  s.rot = rot;
+  s.n_axes = n_axes;
+  s.interleaved = interleaved != 0;
+  int64_t sum = 0;
+  for (int i = 0; i < n_axes; ++i) {
+    s.sections[i] = sections ? sections[i] : rot / 2;
+    if (s.sections[i] < 0) return INFLLM2_ERR_INVALID_ARG;
+    sum += s.sections[i];
+  }
+  if (sum != rot / 2) return INFLLM2_ERR_INVALID_ARG;
+  for (int i = 0; i < rot / 2; ++i) {
+    const long double f = inv_freq ? static_cast<long double>(inv_freq[i])
+                                   : powl(static_cast<long double>(base), -2.0L * i / rot);
+    if (!(fabsl(f) < 1e15L)) return INFLLM2_ERR_INVALID_ARG;
+    long double turn = f / (2.0L * 3.141592653589793238462643383279502884L);
+    turn -= floorl(turn);                        // positions are integers: whole turns drop out
+    // 2^64 * turn, rounded; a fraction that rounds up to a whole turn is 0
+    const long double scaled = floorl(ldexpl(turn, 64) + 0.5L);
+    s.turns[i] = scaled >= 18446744073709551616.0L ? 0 : static_cast<uint64_t>(scaled);
+  }
+  *r = s;
+  return INFLLM2_OK;
+}
+
+static int rope_common(const void* q, const void* k, int32_t dtype, const int32_t* pos, int64_t total, int32_t h_q,
+                       int32_t h_kv, int32_t d, const infllm2_rope_spec* r, void* q_out, void* k_out, int back,
+                       void* stream) {
+  if (!q || !k || !pos || !r || !q_out || !k_out || !aligned16(q) || !aligned16(k) || !aligned16(q_out) ||
+      !aligned16(k_out) || (reinterpret_cast<uintptr_t>(pos) & 3u))
+    return INFLLM2_ERR_INVALID_ARG;
+  if (dtype != INFLLM2_OUT_BF16 && dtype != INFLLM2_OUT_F32) return INFLLM2_ERR_INVALID_ARG;
+  if (total < 0 || h_q <= 0 || h_kv <= 0) return INFLLM2_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return INFLLM2_ERR_UNSUPPORTED;
+  if (total > INT32_MAX || total * (static_cast<int64_t>(h_q) + h_kv) > INT32_MAX) return INFLLM2_ERR_UNSUPPORTED;
+  if (r->rot < 2 || (r->rot & 1) || r->rot > d || r->n_axes < 1 || r->n_axes > INFLLM2_ROPE_MAX_AXES)
+    return INFLLM2_ERR_INVALID_ARG;
+  rope::Args a;
+  a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out; a.pos = pos;
+  a.total = static_cast<int32_t>(total); a.h_q = h_q; a.h_kv = h_kv; a.d = d; a.rot = r->rot; a.n_axes = r->n_axes;
+  a.back = back;
+  int64_t at = 0;
+  for (int i = 0; i < INFLLM2_ROPE_MAX_AXES; ++i) {
+    if (i < r->n_axes && r->sections[i] < 0) return INFLLM2_ERR_INVALID_ARG;
+    at += i < r->n_axes ? r->sections[i] : 0;
+    if (i < INFLLM2_ROPE_MAX_AXES - 1) a.bound[i] = static_cast<int32_t>(std::min<int64_t>(at, INT32_MAX));
+  }
+  if (at != r->rot / 2) return INFLLM2_ERR_INVALID_ARG;
+  memcpy(a.turns, r->turns, sizeof(a.turns));
+  cudaError_t e = launch_rope(a, r->interleaved != 0, dtype == INFLLM2_OUT_F32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INFLLM2_OK : cuda_fail(e);
+}
+
+int infllm2_rope(const void* q, const void* k, int32_t dtype, const int32_t* pos, int64_t total, int32_t h_q,
+                 int32_t h_kv, int32_t d, const infllm2_rope_spec* r, void* q_out, void* k_out, void* stream) {
+  return rope_common(q, k, dtype, pos, total, h_q, h_kv, d, r, q_out, k_out, 0, stream);
+}
+
+int infllm2_rope_backward(const void* dq_rot, const void* dk_rot, int32_t dtype, const int32_t* pos, int64_t total,
+                          int32_t h_q, int32_t h_kv, int32_t d, const infllm2_rope_spec* r, void* dq, void* dk,
+                          void* stream) {
+  return rope_common(dq_rot, dk_rot, dtype, pos, total, h_q, h_kv, d, r, dq, dk, 1, stream);
+}
+
+static int check_paged_cache(const infllm2_paged_cache* c) {
+  if (!c || !c->k_pages || !c->v_pages || !c->block_table || !aligned16(c->k_pages) || !aligned16(c->v_pages) ||
+      (reinterpret_cast<uintptr_t>(c->block_table) & 3u))
+    return INFLLM2_ERR_INVALID_ARG;
+  if (c->dtype != INFLLM2_KV_BF16 && c->dtype != INFLLM2_KV_E4M3) return INFLLM2_ERR_INVALID_ARG;
+  if (c->dtype == INFLLM2_KV_E4M3 &&
+      (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
+    return INFLLM2_ERR_INVALID_ARG;
+  if (c->batch < 1 || c->batch > 65535 || c->n_pages < 1 || c->max_pages < 1 || c->h_kv < 1 || c->page_size < 1)
+    return INFLLM2_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return INFLLM2_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return INFLLM2_ERR_UNSUPPORTED;
+  // positions stay in 31 bits, units of 16 tokens past the end included
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - 1024) return INFLLM2_ERR_UNSUPPORTED;
+  return INFLLM2_OK;
+}
+
+static int page_shift(const infllm2_paged_cache* c) {
+  int s = 4;
+  while ((1 << s) < c->page_size) ++s;
+  return s;
+}
+
+static int paged_rows(const infllm2_paged_cache* c, const void* K, const void* V, void* Ko, void* Vo,
+                      const int32_t* start, const int32_t* cu_seqlens, int64_t total, void* stream) {
+  int r;
+  if ((r = check_paged_cache(c))) return r;
+  const void* k = K ? K : Ko;
+  const void* v = V ? V : Vo;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || total < 0) return INFLLM2_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+    return INFLLM2_ERR_INVALID_ARG;
+  if (!cu_seqlens && total != c->batch) return INFLLM2_ERR_INVALID_ARG;
+  if (total > INT32_MAX || total * c->h_kv > INT32_MAX) return INFLLM2_ERR_UNSUPPORTED;
+  paged::Args a;
+  a.k_pages = static_cast<uint8_t*>(c->k_pages); a.v_pages = static_cast<uint8_t*>(c->v_pages);
+  a.k_scale = c->k_scale; a.v_scale = c->v_scale; a.table = c->block_table; a.cu = cu_seqlens; a.start = start;
+  a.n_pages = c->n_pages; a.page_shift = page_shift(c); a.batch = c->batch; a.max_pages = c->max_pages;
+  a.h_kv = c->h_kv; a.total = static_cast<int32_t>(total);
+  cudaError_t e = launch_paged_rows(a, c->d, c->dtype == INFLLM2_KV_E4M3, K, V, Ko, Vo,
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? INFLLM2_OK : cuda_fail(e);
+}
+
+int infllm2_paged_write(const infllm2_paged_cache* c, const void* K, const void* V, const int32_t* start,
+                        const int32_t* cu_seqlens, int64_t total, void* stream) {
+  if (!K || !V || !start) return INFLLM2_ERR_INVALID_ARG;
+  return paged_rows(c, K, V, nullptr, nullptr, start, cu_seqlens, total, stream);
+}
+
+int infllm2_paged_read(const infllm2_paged_cache* c, void* K, void* V, const int32_t* cu_seqlens, int64_t total,
+                       void* stream) {
+  if (!K || !V || !cu_seqlens) return INFLLM2_ERR_INVALID_ARG;
+  return paged_rows(c, nullptr, nullptr, K, V, nullptr, cu_seqlens, total, stream);
+}
+
+static int check_paged_heads(const infllm2_paged_cache* c, int32_t h_q) {
+  int r;
+  if ((r = check_paged_cache(c)) || (r = check_heads(h_q, c->h_kv, c->d))) return r;
+  if (static_cast<int64_t>(c->batch) * h_q > INT32_MAX) return INFLLM2_ERR_UNSUPPORTED;
+  return INFLLM2_OK;
+}
+
+size_t infllm2_paged_workspace_bytes(const infllm2_paged_cache* c, int32_t h_q) {
+  if (check_paged_heads(c, h_q)) return 0;
+  return pattn::plan(c->batch, h_q / c->h_kv, c->d, num_sms()).bytes;
+}
+
+int infllm2_paged_decode_attn(const infllm2_paged_cache* c, const void* q, int32_t h_q, const int32_t* seq_len,
+                              void* out, int32_t out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                              const infllm2_params* p, void* stream) {
+  int r;
+  if ((r = check_paged_heads(c, h_q)) || (r = check_params(p))) return r;
+  if (!q || !seq_len || !out || !workspace || !aligned16(q) || !aligned16(out) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(seq_len) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return INFLLM2_ERR_INVALID_ARG;
+  if (out_dtype != INFLLM2_OUT_BF16 && out_dtype != INFLLM2_OUT_F32) return INFLLM2_ERR_INVALID_ARG;
+  if (workspace_bytes < infllm2_paged_workspace_bytes(c, h_q)) return INFLLM2_ERR_WORKSPACE_TOO_SMALL;
+  pattn::Args a;
+  a.k_pages = static_cast<const uint8_t*>(c->k_pages); a.v_pages = static_cast<const uint8_t*>(c->v_pages);
+  a.k_scale = c->k_scale; a.v_scale = c->v_scale; a.table = c->block_table; a.len = seq_len;
+  a.q = static_cast<const __nv_bfloat16*>(q); a.out = out; a.lse = lse;
+  a.n_pages = c->n_pages; a.page_shift = page_shift(c); a.batch = c->batch; a.max_pages = c->max_pages;
+  a.h_kv = c->h_kv; a.G = h_q / c->h_kv; a.ctas = num_sms(); a.out_f32 = out_dtype == INFLLM2_OUT_F32;
+  a.scale_log2 = softmax_scale(p, c->d) * dec::kLog2e;
+  cudaError_t e = launch_paged_attn(a, c->d, c->dtype == INFLLM2_KV_E4M3, workspace, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? INFLLM2_OK : cuda_fail(e);
 }
 
