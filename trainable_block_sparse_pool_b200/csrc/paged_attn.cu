@@ -4,44 +4,53 @@
 //
 // For query head h of kv group g and the first n = len[b] positions u,
 //   z_u = scale log2(e) q_h . k_u,  lse = log2 sum_u 2^z_u,  out = sum_u 2^(z_u - lse) v_u,
-// in one pass with a running maximum and sum.  Every key and value is read once
-// for the group's G <= 16 query heads, so the kernel is bound by HBM; 4 d G
-// flop a (token, kv head) go to warp-level mma.sync m16n8k16, whose 16 rows are
-// the group's heads.
+// in one pass with a running reference maximum and sum.  Every key and value is
+// read once for the group's G <= 16 query heads, so HBM is the bound; 4 d G flop
+// a (token, kv head) go to warp-level mma.sync m16n8k16 in the transposed form
+//   S^T [16 tokens x 8 heads] = K Q^T,   O^T [16 columns x 8 heads] += V^T P^T,
+// so groups of at most 8 heads need half the products of larger ones (NH = 1 or
+// 2 tiles of heads).
 //
 // Split.  Lengths are known on the device only, so the grid is fixed (one CTA
-// an SM, kWarps warps) and every warp works alone: the 16-token units of all
-// (sequence, kv head) pairs, in order, are cut into equal ranges, one a warp,
-// whatever the lengths.  A piece of a pair that begins and ends within one
-// range is written out by its warp; the others leave a normalised partial and
-// its log-sum-exp in the workspace, and a second kernel (programmatic dependent
-// launch) joins them in ascending order.  Nothing waits on another CTA.
+// an SM) and every warp works alone: the 16-token units of all (sequence, kv
+// head) pairs, in order, are cut into equal ranges, one a warp, whatever the
+// lengths.  A piece of a pair that begins and ends within one range is written
+// out by its warp; the others leave a normalised partial and its log-sum-exp in
+// the workspace, and a second kernel (programmatic dependent launch) joins them
+// in ascending order.  Nothing waits on another CTA.
 //
 // A warp streams tiles of 8 KB (K and V of 16, 32 or 64 tokens) through its own
-// kStages-deep cp.async ring.  Rows past the piece are filled with zeros, not
-// read, so what lies in unwritten slots never enters a product.
+// kStages-deep cp.async ring, the page numbers of a tile fetched one tile ahead
+// of its copies.  Rows past the piece are filled with zeros, not read, so what
+// lies in unwritten slots never enters a product.
 //
 // 8 bits.  K and V go from e4m3 to f16 exactly.  q is scaled to f16 by a power
 // of two a head (its 8 significant bits are kept down to 2^-29 of the head's
 // largest element, and 2^-39 of it absolutely).  A value's scale multiplies its
-// probability: w_u = p_u * scale_u / R * 2^15 in f16, with R a power of two no
-// less than any scale seen, so w keeps 11 bits where p_u scale_u >= 2^-29 R.
+// probability: w_u = p_u * scale_u / R * 2^11 in f16, with R a power of two no
+// less than any scale seen and p_u <= 2^kMargin, so w keeps 11 bits where
+// p_u scale_u >= 2^-25 R.
 #include "sm100.cuh"
 
 namespace infllm2 {
 
 namespace pattn {
 
-using dec::QFrag;
 using dec::cp_async_commit;
 using dec::cp_async_wait_n;
 using dec::ldsm_x4_t;
-using dec::load_qfrag;
 using dec::mma16816;
 
-constexpr int kWarps = 8;
-constexpr int kStages = 3;
+#ifndef INFLLM2_PATTN_WARPS
+#define INFLLM2_PATTN_WARPS 8
+#endif
+#ifndef INFLLM2_PATTN_STAGES
+#define INFLLM2_PATTN_STAGES 3
+#endif
+constexpr int kWarps = INFLLM2_PATTN_WARPS;
+constexpr int kStages = INFLLM2_PATTN_STAGES;
 constexpr int kUnit = 16;           // tokens; every page size is a multiple of it
+constexpr float kMargin = 4.f;      // the reference maximum is raised only past this many log2 units
 constexpr int kHalf = 4096;         // bytes of K, and of V, in a stage
 
 __device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -55,6 +64,9 @@ __device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[
 __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -65,10 +77,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ float lds32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+// transpose of an 8x8 matrix of 16-bit elements held two a lane
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -117,28 +130,30 @@ struct Cfg {
   static constexpr int kScale = F8 ? 8 * kTile : 0;   // bytes of scales in a stage
   static constexpr int kStage = 2 * kHalf + kScale;
   static constexpr int kSmem = kWarps * kStages * kStage;
-  static constexpr int NT = kTile / 8;                // 8-key tiles of S
-  static constexpr int OT = D / 8;                    // 8-column tiles of O
+  static constexpr int S = kTile / 8;                 // consecutive tokens of a lane group
+  static constexpr int MT = kTile / 16;               // 16-token tiles of S^T
+  static constexpr int DT = D / 16;                   // 16-column tiles of O^T
 };
 
-// Shared-memory byte of 16-byte piece c of tile row r.  Rows of 128 bytes or
-// more keep their own lines with the piece XORed by the row; two 64-byte rows
-// share a line, XORed by the line.
-template <int CH>
-__device__ __forceinline__ uint32_t piece_at(int r, int c) {
-  if (CH >= 8) return r * (CH * 16) + ((c ^ (r & 7)) << 4);
-  return (r >> 1) * 128 + (((r & 1) * 4 + (c ^ ((r >> 1) & 3))) << 4);
+// Row R = g + 8h (g < 8, h < 2) of the tile's S^T tile m is its token S g + 2 m + h: the
+// order is free (probabilities and values use the same one), and this one gives
+// lane group g the S consecutive tokens from S g on, so its scales are vectors.
+template <int S>
+__device__ __forceinline__ int row_token(int m, int R) {
+  return S * (R & 7) + 2 * m + (R >> 3);
 }
 
-// Key n of an 8-key tile of S is the tile's token key_token(n).  The order is
-// free (probabilities and values use the same one); this one lets the eight
-// lanes of each shared-memory phase, two keys of four pieces or four values of
-// two, meet all eight 16-byte banks groups.
-template <int CH>
-__device__ __forceinline__ int key_token(int n) {
-  const int t = n >> 1, e = n & 1;
-  if (CH >= 8) return (2 * t + (t >> 1)) ^ (4 * e);
-  return ((t & 1) | ((t & 2) << 1)) ^ (3 * e);
+// Shared-memory byte of 16-byte piece c of the tile's token S g + x.  Rows of 128
+// bytes or more have lines of their own, the piece XORed with a number made of
+// g; two 64-byte rows (g and g ^ 1) share a line.  The XOR numbers let the eight
+// lanes of each shared-memory phase (K: two lane groups' rows, four pieces
+// each; V: four rows, two pieces each, or eight rows of an ldmatrix) meet all banks.
+template <int CH, int S, bool F8>
+__device__ __forceinline__ uint32_t piece_at(int g, int x, int c) {
+  if (CH == 4)
+    return ((g >> 1) * S + x) * 128 + (((g & 1) ^ ((g >> 1) & 1)) << 6) + ((c ^ ((g >> 2) << 1)) << 4);
+  const int f = F8 ? (((g & 1) << 2) ^ (g & 6)) : (((g & 1) << 2) | (g >> 1));
+  return (g * S + x) * (CH * 16) + ((c ^ f) << 4);
 }
 
 // Walks the tiles of a warp's range.
@@ -170,81 +185,97 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
   return true;
 }
 
+// the page of every 16-token group of the walk's tile (-1: no token of the piece in it)
+template <int kTile>
+__device__ __forceinline__ void fetch_pages(const Args& a, const Walk& w, int (&page)[kTile / kUnit]) {
+  const int32_t* row = a.table + static_cast<int64_t>(w.b) * a.max_pages;
+#pragma unroll
+  for (int i = 0; i < kTile / kUnit; ++i)
+    page[i] = w.u + i < w.ue ? __ldg(row + ((w.u + i) >> (a.page_shift - 4))) : -1;
+}
+
 template <int D, bool F8>
-__device__ __forceinline__ void issue_tile(const Args& a, const Walk& w, uint32_t stage, int lane) {
+__device__ __forceinline__ void issue_tile(const Args& a, const Walk& w, const int (&page)[Cfg<D, F8>::kTile / kUnit],
+                                           uint32_t stage, int lane) {
   using C = Cfg<D, F8>;
-  constexpr int RPI = 32 / C::CH;   // rows an instruction
+  constexpr int NG = C::kTile / kUnit;   // 16-token groups
+  constexpr int IPG = 8 / NG;            // instructions a group: 512 contiguous bytes each
   const int tok0 = w.u * kUnit;
   const int nv = min(C::kTile, w.tok_end - tok0);
-  const int32_t* row = a.table + static_cast<int64_t>(w.b) * a.max_pages;
-  const int r0 = lane / C::CH, c = lane % C::CH;
-  const int mask = (1 << a.page_shift) - 1;
-  int64_t base[C::kTile / kUnit];   // first row of each 16-token group (-1: nothing to read)
+  const int mask = (1 << (a.page_shift - 4)) - 1;
+  const int r0 = lane / C::CH, c = lane % C::CH;   // instruction i: tokens S i + r0
+  int64_t at[NG];                        // first row of the group
+  bool ok = nv == C::kTile;
 #pragma unroll
-  for (int i = 0; i < C::kTile / kUnit; ++i) {
-    const int tok = tok0 + i * kUnit;
-    base[i] = -1;
-    if (i * kUnit < nv) {
-      const int page = __ldg(row + (tok >> a.page_shift));
-      if (page >= 0 && page < a.n_pages)
-        base[i] = ((static_cast<int64_t>(page) * a.h_kv + w.g) << a.page_shift) + (tok & mask);
-      else
-        record_status(INFLLM2_ERR_DEVICE_BOUNDS);
+  for (int i = 0; i < NG; ++i) {
+    at[i] = ((static_cast<int64_t>(page[i]) * a.h_kv + w.g) << a.page_shift) + (((w.u + i) & mask) << 4);
+    ok = ok && page[i] >= 0 && page[i] < a.n_pages;
+  }
+  if (ok) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t off = at[i / IPG] * C::kRow + (i % IPG) * 512 + lane * 16;
+      const uint32_t dst = stage + piece_at<C::CH, C::S, F8>(i, r0, c);
+      cp_async16_full(dst, a.k_pages + off);
+      cp_async16_full(dst + kHalf, a.v_pages + off);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int pg = page[i / IPG];
+      const bool in = C::S * i + r0 < nv, good = pg >= 0 && pg < a.n_pages;
+      if (in && !good) record_status(INFLLM2_ERR_DEVICE_BOUNDS);
+      const int64_t off = in && good ? at[i / IPG] * C::kRow + (i % IPG) * 512 + lane * 16 : 0;
+      const uint32_t dst = stage + piece_at<C::CH, C::S, F8>(i, r0, c);
+      cp_async16_part(dst, a.k_pages + off, in && good ? 16 : 0);
+      cp_async16_part(dst + kHalf, a.v_pages + off, in && good ? 16 : 0);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * RPI + r0;
-    const int64_t at = base[i * RPI / kUnit];
-    const bool ok = r < nv && at >= 0;
-    const int64_t off = ok ? (at + (r & (kUnit - 1))) * C::kRow + c * 16 : 0;
-    const uint32_t dst = stage + piece_at<C::CH>(r, c);
-    cp_async16_part(dst, a.k_pages + off, ok ? 16 : 0);
-    cp_async16_part(dst + kHalf, a.v_pages + off, ok ? 16 : 0);
-  }
-  if (F8) {
+  if constexpr (F8) {
     // scales: pieces of four tokens, K's then V's
     constexpr int P = C::kTile / 4;
     if (lane < 2 * P) {
       const int t = 4 * (lane % P);
-      int64_t at = -1;
+      int64_t row = at[0];
+      int pg = page[0];
 #pragma unroll
-      for (int i = 0; i < C::kTile / kUnit; ++i)
-        if (t / kUnit == i) at = base[i];
-      const int bytes = at >= 0 ? max(0, min(16, 4 * (nv - t))) : 0;
+      for (int i = 1; i < NG; ++i)
+        if (t / kUnit == i) { row = at[i]; pg = page[i]; }
+      const int bytes = pg >= 0 && pg < a.n_pages ? max(0, min(16, 4 * (nv - t))) : 0;
       const float* src = lane < P ? a.k_scale : a.v_scale;
-      cp_async16_part(stage + 2 * kHalf + lane * 16, bytes > 0 ? src + at + (t & (kUnit - 1)) : src, bytes);
+      cp_async16_part(stage + 2 * kHalf + lane * 16, bytes > 0 ? src + row + (t & (kUnit - 1)) : src, bytes);
     }
   }
 }
 
-// Query heads as A fragments: bf16 as they are, or (F8) f16 scaled to
-// [2^14, 2^15) by a power of two a head; `unscale` undoes it.
-template <int D, bool F8>
+// Query heads as B fragments (head gid + 8 nh): bf16 as they are, or (F8) f16
+// scaled to [2^14, 2^15) by a power of two a head; `unscale` (of this lane's
+// score columns, heads 2 tig + e + 8 nh) undoes it and carries the softmax scale.
+template <int D, bool F8, int NH>
 struct Query {
-  uint32_t a[D / 16][4];
-  float unscale[2];
+  uint32_t b[NH][D / 16][2];
+  float s[NH][2];
 };
 
-template <int D, bool F8>
-__device__ __forceinline__ void load_query(Query<D, F8>& f, const __nv_bfloat16* q, int lane, int G) {
+template <int D, bool F8, int NH>
+__device__ __forceinline__ void load_query(Query<D, F8, NH>& f, const __nv_bfloat16* q, int lane, int G,
+                                           float scale_log2) {
   const int gid = lane >> 2, tig = lane & 3;
-  if (!F8) {
-    QFrag<D> t;
-    load_qfrag<D>(t, q, lane, G);
 #pragma unroll
-    for (int p = 0; p < D / 32; ++p) {
-      f.a[2 * p][0] = t.lo[p].x; f.a[2 * p][1] = t.hi[p].x; f.a[2 * p][2] = t.lo[p].y; f.a[2 * p][3] = t.hi[p].y;
-      f.a[2 * p + 1][0] = t.lo[p].z; f.a[2 * p + 1][1] = t.hi[p].z;
-      f.a[2 * p + 1][2] = t.lo[p].w; f.a[2 * p + 1][3] = t.hi[p].w;
+  for (int nh = 0; nh < NH; ++nh) {
+    const int h = gid + 8 * nh;
+    if (!F8) {
+      // pieces of 8: k steps 2j and 2j + 1 cover d = 8 (tig + 4j) + {0, 1, 2, 3} and + {4, 5, 6, 7} in this lane
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const uint4 v = h < G ? *reinterpret_cast<const uint4*>(q + h * D + 8 * (tig + 4 * j)) : make_uint4(0, 0, 0, 0);
+        f.b[nh][2 * j][0] = v.x; f.b[nh][2 * j][1] = v.y;
+        f.b[nh][2 * j + 1][0] = v.z; f.b[nh][2 * j + 1][1] = v.w;
+      }
+      f.s[nh][0] = f.s[nh][1] = scale_log2;
+      continue;
     }
-    f.unscale[0] = f.unscale[1] = 1.f;
-    return;
-  }
-  // k step 4j + i covers d = 16 (tig + 4j) + 4i + {0, 1} and + {2, 3} in this thread
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int h = gid + 8 * s;
+    // pieces of 16: k step 4j + i covers d = 16 (tig + 4j) + 4i + {0, 1, 2, 3} in this lane
     uint4 v[D / 32];
     uint32_t top = 0;
 #pragma unroll
@@ -257,235 +288,282 @@ __device__ __forceinline__ void load_query(Query<D, F8>& f, const __nv_bfloat16*
     top = max(top & 0xffffu, top >> 16);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // bf16 exponent e: |q| < 2^(e - 126); scale by 2^(141 - e)
+    // bf16 exponent e: |q| < 2^(e - 126); scaled by 2^(141 - e)
     const int e = min(max(static_cast<int>(top >> 7), 15), 254);
     const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-    f.unscale[s] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+    const float un = __uint_as_float(static_cast<uint32_t>(e - 14) << 23) * scale_log2;
+    f.s[nh][0] = __shfl_sync(0xffffffffu, un, 8 * tig);
+    f.s[nh][1] = __shfl_sync(0xffffffffu, un, 8 * tig + 4);
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4& x = v[2 * j + (i >> 1)];
         const uint32_t w0 = (i & 1) ? x.z : x.x, w1 = (i & 1) ? x.w : x.y;
-        f.a[4 * j + i][s] = pack_f16(__uint_as_float(w0 << 16) * up, __uint_as_float(w0 & 0xffff0000u) * up);
-        f.a[4 * j + i][2 + s] = pack_f16(__uint_as_float(w1 << 16) * up, __uint_as_float(w1 & 0xffff0000u) * up);
+        f.b[nh][4 * j + i][0] = pack_f16(__uint_as_float(w0 << 16) * up, __uint_as_float(w0 & 0xffff0000u) * up);
+        f.b[nh][4 * j + i][1] = pack_f16(__uint_as_float(w1 << 16) * up, __uint_as_float(w1 & 0xffff0000u) * up);
       }
   }
 }
 
-template <int D, bool F8>
+// This lane's columns: heads 2 tig + e + 8 nh.
+template <int D, bool F8, int NH>
 struct State {
-  float o[D / 8][4];
-  float m[2], l[2];   // running maximum (all four lanes of a head) and this lane's sum, heads gid and gid + 8
-  int e_r;            // F8: R = 2^(e_r - 127)
+  float o[NH][D / 16][4];   // O^T tiles: rows gid and gid + 8
+  float m[NH][2];           // reference maximum, log2 units (the same in all lanes of a head)
+  float l[NH][2];           // this lane's share of the sum
+  int e_r;                  // F8: R = 2^(e_r - 127)
 };
 
-template <int D, bool F8>
-__device__ __forceinline__ void state_clear(State<D, F8>& s) {
+template <int D, bool F8, int NH>
+__device__ __forceinline__ void state_clear(State<D, F8, NH>& s) {
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
-  s.m[0] = s.m[1] = -INFINITY;
-  s.l[0] = s.l[1] = 0.f;
+  for (int nh = 0; nh < NH; ++nh) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) s.o[nh][i][0] = s.o[nh][i][1] = s.o[nh][i][2] = s.o[nh][i][3] = 0.f;
+    s.m[nh][0] = s.m[nh][1] = -INFINITY;
+    s.l[nh][0] = s.l[nh][1] = 0.f;
+  }
   s.e_r = 16;
 }
 
-template <int D, bool F8>
-__device__ __forceinline__ void attend_tile(State<D, F8>& st, const Query<D, F8>& q, uint32_t stage, int nv,
-                                            float scale_log2, int lane) {
+template <int D, bool F8, int NH>
+__device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D, F8, NH>& q, uint32_t stage, int nv,
+                                            int lane) {
   using C = Cfg<D, F8>;
   const int gid = lane >> 2, tig = lane & 3;
-  float z[C::NT][4];
-  // S = Q K^T
+  float z[C::MT][NH][4];
+  // S^T = K Q^T
 #pragma unroll
-  for (int t = 0; t < C::NT; ++t) {
-    z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
-    const int r = 8 * t + key_token<C::CH>(gid);
+  for (int m = 0; m < C::MT; ++m) {
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) z[m][nh][0] = z[m][nh][1] = z[m][nh][2] = z[m][nh][3] = 0.f;
 #pragma unroll
     for (int j = 0; j < C::CH / 4; ++j) {
-      const uint4 k = lds128(stage + piece_at<C::CH>(r, tig + 4 * j));
+      const uint4 k0 = lds128(stage + piece_at<C::CH, C::S, F8>(gid, 2 * m, tig + 4 * j));
+      const uint4 k1 = lds128(stage + piece_at<C::CH, C::S, F8>(gid, 2 * m + 1, tig + 4 * j));
       if (F8) {
-        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma16816_f16(z[t], q.a[4 * j + i], paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w[i])),
-                       paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t f[4] = {paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w0[i])),
+                                 paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w1[i])),
+                                 paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w0[i] >> 16)),
+                                 paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w1[i] >> 16))};
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) mma16816_f16(z[m][nh], f, q.b[nh][4 * j + i][0], q.b[nh][4 * j + i][1]);
+        }
       } else {
-        mma16816(z[t], q.a[2 * j], k.x, k.y);
-        mma16816(z[t], q.a[2 * j + 1], k.z, k.w);
+        const uint32_t f0[4] = {k0.x, k1.x, k0.y, k1.y}, f1[4] = {k0.z, k1.z, k0.w, k1.w};
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+          mma16816(z[m][nh], f0, q.b[nh][2 * j][0], q.b[nh][2 * j][1]);
+          mma16816(z[m][nh], f1, q.b[nh][2 * j + 1][0], q.b[nh][2 * j + 1][1]);
+        }
       }
     }
   }
-  // scale and mask; the tile's maxima
-  const int n0 = key_token<C::CH>(2 * tig), n1 = key_token<C::CH>(2 * tig + 1);
-  const float s0 = scale_log2 * q.unscale[0], s1 = scale_log2 * q.unscale[1];
-  float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-  for (int t = 0; t < C::NT; ++t) {
-    float f0 = 1.f, f1 = 1.f;
-    if (F8) {
-      f0 = lds32(stage + 2 * kHalf + 4 * (8 * t + n0));
-      f1 = lds32(stage + 2 * kHalf + 4 * (8 * t + n1));
-    }
-    const bool in0 = 8 * t + n0 < nv, in1 = 8 * t + n1 < nv;
-    z[t][0] = in0 ? z[t][0] * (s0 * f0) : -INFINITY;
-    z[t][1] = in1 ? z[t][1] * (s0 * f1) : -INFINITY;
-    z[t][2] = in0 ? z[t][2] * (s1 * f0) : -INFINITY;
-    z[t][3] = in1 ? z[t][3] * (s1 * f1) : -INFINITY;
-    top[0] = fmaxf(top[0], fmaxf(z[t][0], z[t][1]));
-    top[1] = fmaxf(top[1], fmaxf(z[t][2], z[t][3]));
-  }
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    top[s] = fmaxf(top[s], __shfl_xor_sync(0xffffffffu, top[s], 1));
-    top[s] = fmaxf(top[s], __shfl_xor_sync(0xffffffffu, top[s], 2));
-  }
-  float back = 1.f;   // F8: R before / R now
+  // the keys' scales; the values' scales
+  float vs[F8 ? C::S : 1];
   if constexpr (F8) {
-    uint32_t bits = 0;
+    float ks[C::S];
 #pragma unroll
-    for (int i = 0; i < C::kTile / 32; ++i)
-      bits = max(bits, __float_as_uint(lds32(stage + 2 * kHalf + 4 * C::kTile + 4 * (lane + 32 * i))) & 0x7fffffffu);
-    bits = __reduce_max_sync(0xffffffffu, bits);
-    const int e = min(max(static_cast<int>((bits + 0x7fffffu) >> 23), 16), 250);
-    if (e > st.e_r) {
+    for (int i = 0; i < C::S / 4; ++i) {
+      const uint4 k = lds128(stage + 2 * kHalf + 4 * C::S * gid + 16 * i);
+      const uint4 v = lds128(stage + 2 * kHalf + 4 * C::kTile + 4 * C::S * gid + 16 * i);
+      ks[4 * i] = __uint_as_float(k.x); ks[4 * i + 1] = __uint_as_float(k.y);
+      ks[4 * i + 2] = __uint_as_float(k.z); ks[4 * i + 3] = __uint_as_float(k.w);
+      vs[4 * i] = __uint_as_float(v.x); vs[4 * i + 1] = __uint_as_float(v.y);
+      vs[4 * i + 2] = __uint_as_float(v.z); vs[4 * i + 3] = __uint_as_float(v.w);
+    }
+#pragma unroll
+    for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[m][nh][e] *= ks[2 * m + (e >> 1)];
+  }
+  if (nv < C::kTile) {
+#pragma unroll
+    for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (C::S * gid + 2 * m + (e >> 1) >= nv) z[m][nh][e] = -INFINITY;
+  }
+  // raise the reference maximum (and R) where a score (a scale) passes it
+  float top[NH][2];
+  bool past = false;
+#pragma unroll
+  for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float t = -INFINITY;
+#pragma unroll
+      for (int m = 0; m < C::MT; ++m) t = fmaxf(t, fmaxf(z[m][nh][e], z[m][nh][2 + e]));
+      top[nh][e] = t * q.s[nh][e];
+      past = past || top[nh][e] > st.m[nh][e] + kMargin;
+    }
+  float vtop = 0.f;
+  if constexpr (F8) {
+#pragma unroll
+    for (int i = 0; i < C::S; ++i) vtop = fmaxf(vtop, fabsf(vs[i]));
+    past = past || vtop > __uint_as_float(static_cast<uint32_t>(st.e_r) << 23);
+  }
+  if (__any_sync(0xffffffffu, past)) {
+    float back = 1.f;   // F8: R before / R now
+    if constexpr (F8) {
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(vtop));
+      const int e = min(max(static_cast<int>((bits + 0x7fffffu) >> 23), st.e_r), 250);
       back = e - st.e_r > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + st.e_r - e) << 23);
       st.e_r = e;
     }
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = top[nh][e];
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+        const float m = fmaxf(st.m[nh][e], t);
+        const float f = st.m[nh][e] == m ? 1.f : ex2(st.m[nh][e] - m);
+        st.m[nh][e] = m;
+        st.l[nh][e] *= f;
+#pragma unroll
+        for (int i = 0; i < C::DT; ++i) {
+          st.o[nh][i][e] *= f * back;
+          st.o[nh][i][2 + e] *= f * back;
+        }
+      }
   }
-  if (__any_sync(0xffffffffu, top[0] > st.m[0] || top[1] > st.m[1] || back != 1.f)) {
-    float f[2];
+  // probabilities: P in bf16 (relative error 2^-9 on a weight; the output itself is
+  // rounded to bf16 or its like), or w in f16; their sums stay in fp32 unrounded
+  if constexpr (F8) {
+    const float up = __uint_as_float(static_cast<uint32_t>(254 + 11 - st.e_r) << 23);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const float m = fmaxf(st.m[s], top[s]);
-      f[s] = st.m[s] == m ? 1.f : ex2(st.m[s] - m);   // equal infinities: nothing summed yet, or NaN below
-      st.m[s] = m;
-      st.l[s] *= f[s];
-      f[s] *= back;
-    }
-#pragma unroll
-    for (int i = 0; i < C::OT; ++i) {
-      st.o[i][0] *= f[0]; st.o[i][1] *= f[0];
-      st.o[i][2] *= f[1]; st.o[i][3] *= f[1];
-    }
+    for (int i = 0; i < C::S; ++i) vs[i] *= up;
   }
-  const float m0 = st.m[0] == -INFINITY ? 0.f : st.m[0], m1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
-  const float up = F8 ? __uint_as_float(static_cast<uint32_t>(254 + 15 - st.e_r) << 23) : 1.f;
-  // probabilities as A fragments: P in bf16 (relative error 2^-9, that of the
-  // output's own rounding), or w in f16; their sums stay in fp32 unrounded
-  uint32_t p[C::NT / 2][4];
+  float neg[NH][2];
 #pragma unroll
-  for (int t = 0; t < C::NT; ++t) {
-    float p0 = ex2(z[t][0] - m0), p1 = ex2(z[t][1] - m0), p2 = ex2(z[t][2] - m1), p3 = ex2(z[t][3] - m1);
-    st.l[0] += p0 + p1;
-    st.l[1] += p2 + p3;
+  for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) neg[nh][e] = st.m[nh][e] == -INFINITY ? 0.f : -st.m[nh][e];
+  uint32_t p[C::MT][NH][2];   // B fragments: 16 tokens x 8 heads
+#pragma unroll
+  for (int m = 0; m < C::MT; ++m)
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = ex2(fmaf(z[m][nh][e], q.s[nh][e & 1], neg[nh][e & 1]));
+        st.l[nh][e & 1] += w[e];
+        if constexpr (F8) w[e] *= vs[2 * m + (e >> 1)];
+      }
+      p[m][nh][0] = movmatrix(F8 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
+      p[m][nh][1] = movmatrix(F8 ? pack_f16(w[2], w[3]) : pack_bf16(w[2], w[3]));
+    }
+  // O^T += V^T P^T
+  const uint32_t vb = stage + kHalf;
+#pragma unroll
+  for (int m = 0; m < C::MT; ++m) {
     if (F8) {
-      const float f0 = lds32(stage + 2 * kHalf + 4 * (C::kTile + 8 * t + n0)) * up;
-      const float f1 = lds32(stage + 2 * kHalf + 4 * (C::kTile + 8 * t + n1)) * up;
-      p[t >> 1][2 * (t & 1)] = pack_f16(p0 * f0, p1 * f1);
-      p[t >> 1][2 * (t & 1) + 1] = pack_f16(p2 * f0, p3 * f1);
-    } else {
-      p[t >> 1][2 * (t & 1)] = pack_bf16(p0, p1);
-      p[t >> 1][2 * (t & 1) + 1] = pack_bf16(p2, p3);
-    }
-  }
-  // O += P V
-  const uint32_t vs = stage + kHalf;
-#pragma unroll
-  for (int k = 0; k < C::NT / 2; ++k) {
-    if (F8) {
-      // a byte of four value rows: column d = 16 gid + i (8 gid + i for d = 64) of O's tile i
-      const int r0 = 16 * k + n0, r1 = 16 * k + n1;
+      // bytes of four rows: column D/8 gid + 2 i + {0, 1} is row gid, gid + 8 of O^T's tile i
       constexpr int W = D / 32;   // words a row and lane
       uint32_t w[4][W];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = (i & 1 ? r1 : r0) + (i >> 1) * 8;
+        const int g = 2 * tig + (i & 1), x = 2 * m + (i >> 1);
         if (W == 4) {
-          const uint4 v = lds128(vs + piece_at<C::CH>(r, gid));
+          const uint4 v = lds128(vb + piece_at<C::CH, C::S, F8>(g, x, gid));
           w[i][0] = v.x; w[i][1] = v.y; w[i][W - 2] = v.z; w[i][W - 1] = v.w;
         } else {
-          const uint2 v = lds64(vs + piece_at<C::CH>(r, gid >> 1) + (gid & 1) * 8);
+          const uint2 v = lds64(vb + piece_at<C::CH, C::S, F8>(g, x, gid >> 1) + (gid & 1) * 8);
           w[i][0] = v.x; w[i][1] = v.y;
         }
       }
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const uint32_t lo0 = __byte_perm(w[0][j], w[1][j], 0x5140), lo1 = __byte_perm(w[0][j], w[1][j], 0x7362);
-        const uint32_t hi0 = __byte_perm(w[2][j], w[3][j], 0x5140), hi1 = __byte_perm(w[2][j], w[3][j], 0x7362);
-        mma16816_f16(st.o[4 * j], p[k], paged::e4m3x2_to_f16x2(static_cast<uint16_t>(lo0)),
-                     paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi0)));
-        mma16816_f16(st.o[4 * j + 1], p[k], paged::e4m3x2_to_f16x2(static_cast<uint16_t>(lo0 >> 16)),
-                     paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi0 >> 16)));
-        mma16816_f16(st.o[4 * j + 2], p[k], paged::e4m3x2_to_f16x2(static_cast<uint16_t>(lo1)),
-                     paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi1)));
-        mma16816_f16(st.o[4 * j + 3], p[k], paged::e4m3x2_to_f16x2(static_cast<uint16_t>(lo1 >> 16)),
-                     paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi1 >> 16)));
-      }
-    } else {
-      // four 8x8 matrices: keys 0-7 and 8-15 of the step, two 8-column tiles
-      const int i = lane >> 3;
-      const int r = 16 * k + (i & 1) * 8 + key_token<C::CH>(lane & 7);
+      for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int j = 0; j < C::OT / 2; ++j) {
-        uint32_t v[4];
-        ldsm_x4_t(v, vs + piece_at<C::CH>(r, 2 * j + (i >> 1)));
-        mma16816(st.o[2 * j], p[k], v[0], v[1]);
-        mma16816(st.o[2 * j + 1], p[k], v[2], v[3]);
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t lo = __byte_perm(w[0][j], w[1][j], e ? 0x7362 : 0x5140);
+          const uint32_t hi = __byte_perm(w[2][j], w[3][j], e ? 0x7362 : 0x5140);
+          const uint32_t f[4] = {paged::e4m3x2_to_f16x2(static_cast<uint16_t>(lo)),
+                                 paged::e4m3x2_to_f16x2(static_cast<uint16_t>(lo >> 16)),
+                                 paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi)),
+                                 paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16))};
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) mma16816_f16(st.o[nh][2 * j + e], f, p[m][nh][0], p[m][nh][1]);
+        }
+    } else {
+      // four 8x8 matrices: columns 0-7 and 8-15 of the tile, rows 0-7, then rows 8-15 of the step
+      const int i = lane >> 3;
+#pragma unroll
+      for (int j = 0; j < C::DT; ++j) {
+        uint32_t f[4];
+        ldsm_x4_t(f, vb + piece_at<C::CH, C::S, F8>(lane & 7, 2 * m + (i >> 1), 2 * j + (i & 1)));
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) mma16816(st.o[nh][j], f, p[m][nh][0], p[m][nh][1]);
       }
     }
   }
 }
 
 // The G heads' normalised rows and log-sum-exps: to out and lse (slot < 0), or to partial `slot`.
-template <int D, bool F8>
-__device__ __forceinline__ void write_piece(const Args& a, State<D, F8>& st, int b, int g, int slot, int lane) {
+template <int D, bool F8, int NH>
+__device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st, int b, int g, int64_t slot, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    float l = st.l[s];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const int h = gid + 8 * s;
-    if (h >= a.G) continue;
-    // l = 0: every score was -inf; the row is empty
-    float inv = l == 0.f ? 0.f : 1.f / l;
-    if (F8) inv *= __uint_as_float(static_cast<uint32_t>(st.e_r - 15) << 23);
-    const float lse = l == 0.f ? -INFINITY : st.m[s] + log2f(l);
-    const int64_t row = (static_cast<int64_t>(b) * a.h_kv + g) * a.G + h;
-    float* po = nullptr;
-    if (slot >= 0) {
-      po = a.part_o + (static_cast<int64_t>(slot) * a.G + h) * D;
-      if (tig == 0) a.part_lse[static_cast<int64_t>(slot) * a.G + h] = lse;
-    } else {
-      if (a.out_f32) po = static_cast<float*>(a.out) + row * D;
-      if (a.lse && tig == 0) a.lse[row] = lse;
-    }
-    __nv_bfloat16* pb = static_cast<__nv_bfloat16*>(a.out) + row * D;
-    if (F8) {
-      // this lane: columns [D/4 tig, D/4 (tig + 1)), tiles' first columns, then their second ones
+  for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e) {
+      float l = st.l[nh][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int h = 2 * tig + e + 8 * nh;
+      if (h >= a.G) continue;
+      // l = 0: every score was -inf; the row is empty
+      float inv = l == 0.f ? 0.f : 1.f / l;
+      if (F8) inv *= __uint_as_float(static_cast<uint32_t>(st.e_r - 11) << 23);
+      const float lse = l == 0.f ? -INFINITY : st.m[nh][e] + log2f(l);
+      const int64_t row = (static_cast<int64_t>(b) * a.h_kv + g) * a.G + h;
+      float* po = nullptr;
+      if (slot >= 0) {
+        po = a.part_o + (slot * a.G + h) * D;
+        if (gid == 0) a.part_lse[slot * a.G + h] = lse;
+      } else {
+        if (a.out_f32) po = static_cast<float*>(a.out) + row * D;
+        if (a.lse && gid == 0) a.lse[row] = lse;
+      }
+      __nv_bfloat16* pb = static_cast<__nv_bfloat16*>(a.out) + row * D;
+      if (F8) {
+        // columns D/8 gid .. D/8 (gid + 1)
 #pragma unroll
-        for (int i = 0; i < D / 8; i += 4) {
-          const float v0 = st.o[i][2 * s + e] * inv, v1 = st.o[i + 1][2 * s + e] * inv;
-          const float v2 = st.o[i + 2][2 * s + e] * inv, v3 = st.o[i + 3][2 * s + e] * inv;
-          const int d = D / 4 * tig + D / 8 * e + i;
+        for (int i = 0; i < D / 16; i += 2) {
+          const float v0 = st.o[nh][i][e] * inv, v1 = st.o[nh][i][2 + e] * inv;
+          const float v2 = st.o[nh][i + 1][e] * inv, v3 = st.o[nh][i + 1][2 + e] * inv;
+          const int d = D / 8 * gid + 2 * i;
           if (po) *reinterpret_cast<float4*>(po + d) = make_float4(v0, v1, v2, v3);
           else *reinterpret_cast<uint2*>(pb + d) = make_uint2(pack_bf16(v0, v1), pack_bf16(v2, v3));
         }
-    } else {
+      } else {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const float v0 = st.o[i][2 * s] * inv, v1 = st.o[i][2 * s + 1] * inv;
-        const int d = 8 * i + 2 * tig;
-        if (po) *reinterpret_cast<float2*>(po + d) = make_float2(v0, v1);
-        else *reinterpret_cast<uint32_t*>(pb + d) = pack_bf16(v0, v1);
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float v = st.o[nh][i][2 * r + e] * inv;
+            const int d = 16 * i + 8 * r + gid;
+            if (po) po[d] = v;
+            else pb[d] = __float2bfloat16_rn(v);
+          }
       }
     }
-  }
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int NH>
 __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_constant__ Args a) {
   using C = Cfg<D, F8>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -567,38 +645,38 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
   Walk cons = prod;
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
   bool more = true;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
+  int page[C::kTile / kUnit];
+  fetch_pages<C::kTile>(a, prod, page);
+  auto produce = [&](int slot) {
     if (more) {
-      issue_tile<D, F8>(a, prod, ring + s * C::kStage, lane);
+      issue_tile<D, F8>(a, prod, page, ring + slot * C::kStage, lane);
       more = walk_next<C::kTile>(a, prod);
+      if (more) fetch_pages<C::kTile>(a, prod, page);
     }
     cp_async_commit();
-  }
-  State<D, F8> st;
-  Query<D, F8> q;
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) produce(s);
+  State<D, F8, NH> st;
+  Query<D, F8, NH> q;
   bool first = true;
   int piece_u = 0;
   for (int slot = 0;; slot = slot == kStages - 1 ? 0 : slot + 1) {
     cp_async_wait_n<kStages - 2>();
     __syncwarp();
-    if (more) {
-      issue_tile<D, F8>(a, prod, ring + (slot == 0 ? kStages - 1 : slot - 1) * C::kStage, lane);
-      more = walk_next<C::kTile>(a, prod);
-    }
-    cp_async_commit();
+    produce(slot == 0 ? kStages - 1 : slot - 1);
     if (first) {
-      load_query<D, F8>(q, a.q + (static_cast<int64_t>(cons.b) * a.h_kv + cons.g) * a.G * D, lane, a.G);
+      load_query<D, F8, NH>(q, a.q + (static_cast<int64_t>(cons.b) * a.h_kv + cons.g) * a.G * D, lane, a.G,
+                            a.scale_log2);
       state_clear(st);
       piece_u = cons.u;
     }
-    attend_tile<D, F8>(st, q, ring + slot * C::kStage, min(C::kTile, cons.tok_end - cons.u * kUnit), a.scale_log2,
-                       lane);
+    attend_tile<D, F8, NH>(st, q, ring + slot * C::kStage, min(C::kTile, cons.tok_end - cons.u * kUnit), lane);
     first = cons.u + C::kTile / kUnit >= cons.ue;
     if (first) {
       const bool from0 = piece_u == 0, to_end = cons.ue == cons.n;
       // a range has at most one piece begun in another range and one that goes on into the next
-      write_piece<D, F8>(a, st, cons.b, cons.g, from0 && to_end ? -1 : 2 * wk + (from0 ? 1 : 0), lane);
+      write_piece<D, F8, NH>(a, st, cons.b, cons.g, from0 && to_end ? -1 : 2 * wk + (from0 ? 1 : 0), lane);
     }
     if (!walk_next<C::kTile>(a, cons)) break;
   }
@@ -709,12 +787,12 @@ static Plan plan(int batch, int G, int d, int ctas) {
   return p;
 }
 
-template <int D, bool F8>
-static cudaError_t launch(const Args& a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int D, bool F8, int NH>
+static cudaError_t launch_heads(const Args& a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, F8, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D, F8>::kSmem);
   if (e != cudaSuccess) return e;
-  attend_kernel<D, F8><<<a.ctas, 32 * kWarps, Cfg<D, F8>::kSmem, st>>>(a);
+  attend_kernel<D, F8, NH><<<a.ctas, 32 * kWarps, Cfg<D, F8>::kSmem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -734,6 +812,11 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
   const int by_pair = pairs <= workers;
   return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, a, by_pair, rows)
               : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, by_pair, rows);
+}
+
+template <int D, bool F8>
+static cudaError_t launch(const Args& a, cudaStream_t st) {
+  return a.G > 8 ? launch_heads<D, F8, 2>(a, st) : launch_heads<D, F8, 1>(a, st);
 }
 
 }  // namespace pattn
