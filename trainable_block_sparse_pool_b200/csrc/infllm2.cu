@@ -528,7 +528,7 @@ static int check_paged_heads(const infllm2_paged_cache* c, int32_t h_q) {
 
 size_t infllm2_paged_workspace_bytes(const infllm2_paged_cache* c, int32_t h_q) {
   if (check_paged_heads(c, h_q)) return 0;
-  return pattn::plan(c->batch, h_q / c->h_kv, c->d, num_sms()).bytes;
+  return pattn::plan(h_q / c->h_kv, c->d, num_sms()).bytes;
 }
 
 int infllm2_paged_decode_attn(const infllm2_paged_cache* c, const void* q, int32_t h_q, const int32_t* seq_len,

@@ -12,12 +12,13 @@
 // 2 tiles of heads).
 //
 // Split.  Lengths are known on the device only, so the grid is fixed (one CTA
-// an SM) and every warp works alone: the 16-token units of all (sequence, kv
-// head) pairs, in order, are cut into equal ranges, one a warp, whatever the
-// lengths.  A piece of a pair that begins and ends within one range is written
-// out by its warp; the others leave a normalised partial and its log-sum-exp in
-// the workspace, and a second kernel (programmatic dependent launch) joins them
-// in ascending order.  Nothing waits on another CTA.
+// an SM) and every warp works alone: the tiles of all (sequence, kv head) pairs,
+// in order, each pair with one more for its start and end, are cut into equal
+// ranges, one a warp, whatever the lengths.  A piece of a pair that begins and
+// ends within one range is written out by its warp; the others leave a
+// normalised partial and its log-sum-exp in the workspace, and a second kernel
+// (programmatic dependent launch) joins them in ascending order.  Nothing waits
+// on another CTA.
 //
 // A warp streams tiles of 8 KB (K and V of 16, 32 or 64 tokens) through its own
 // kStages-deep cp.async ring, the page numbers of a tile fetched one tile ahead
@@ -104,23 +105,28 @@ struct Args {
   const __nv_bfloat16* q;
   void* out;
   float* lse;             // [batch, h_q] or null
-  int64_t* prefix;        // workspace: [batch + 1] units of the sequences before b (one kv head)
+  int2* desc;             // workspace: what to join; by pair: (first worker, pieces), by worker: (pair, pieces)
   float* part_o;          // workspace: [2 * workers][G][D]
   float* part_lse;        // workspace: [2 * workers][G]
+  int32_t by_pair;        // at most as many pairs as workers
   int32_t n_pages, page_shift, batch, max_pages, h_kv, G, ctas, out_f32;
   float scale_log2;
 };
 
-// units of a sequence; a length outside [0, capacity] counts as 0 (recorded by CTA 0)
-__device__ __forceinline__ int seq_units(const Args& a, int b) {
+// tiles of a sequence; a length outside [0, capacity] counts as 0 (recorded by CTA 0)
+template <int kTile>
+__device__ __forceinline__ int seq_tiles(const Args& a, int b) {
   const int n = __ldg(a.len + b);
   const bool ok = n >= 0 && n <= static_cast<int64_t>(a.max_pages) << a.page_shift;
   if (!ok && blockIdx.x == 0) record_status(INFLLM2_ERR_DEVICE_BOUNDS);
-  return ok ? (n + kUnit - 1) / kUnit : 0;
+  return ok ? (n + kTile - 1) / kTile : 0;
 }
+// a pair's share of the ranges
+__device__ __forceinline__ int pair_cost(int tiles) { return tiles > 0 ? tiles + 1 : 0; }
 
-// range of worker w of nw over `total` units
-__device__ __forceinline__ int64_t range_begin(int64_t total, int w, int nw) { return total * w / nw; }
+__device__ __forceinline__ int64_t div_pos(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
 
 template <int D, bool F8>
 struct Cfg {
@@ -158,31 +164,37 @@ __device__ __forceinline__ uint32_t piece_at(int g, int x, int c) {
 
 // Walks the tiles of a warp's range.
 struct Walk {
-  int b, g, n, u, ue;   // sequence, kv head, its units, next unit, end of this piece
-  int64_t left;         // units of the range after this piece
+  int b, g, n, t, te;   // sequence, kv head, its tiles, the next one, end of this piece
+  int64_t left;         // cost of the range from the end of this piece on
   int tok_end;          // tokens of the piece end here
 };
 
-__device__ __forceinline__ void walk_piece(const Args& a, Walk& w) {
-  const int64_t take = min(static_cast<int64_t>(w.n - w.u), w.left);
-  w.ue = w.u + static_cast<int>(take);
+// the piece of pair (b, g) from cost position y on; false when the range covers none of its tiles
+template <int kTile>
+__device__ __forceinline__ bool walk_piece(const Args& a, Walk& w, int y) {
+  const int take = static_cast<int>(min(static_cast<int64_t>(w.n + 1 - y), w.left));
   w.left -= take;
-  w.tok_end = min(__ldg(a.len + w.b), w.ue * kUnit);
+  w.t = max(y - 1, 0);
+  w.te = y + take - 1;
+  w.tok_end = min(__ldg(a.len + w.b), w.te * kTile);
+  return w.t < w.te;
+}
+
+// the first piece at or after pair (b, g); false when the range is done
+template <int kTile>
+__device__ __forceinline__ bool walk_pair(const Args& a, Walk& w) {
+  if (w.left <= 0) return false;
+  if (++w.g == a.h_kv) {
+    w.g = 0;
+    do { ++w.b; w.n = seq_tiles<kTile>(a, w.b); } while (w.n == 0);
+  }
+  return walk_piece<kTile>(a, w, 0);   // an empty piece (the pair's start alone) ends its range
 }
 
 // to the next tile; false when the range is done
 template <int kTile>
 __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
-  w.u += kTile / kUnit;
-  if (w.u < w.ue) return true;
-  if (w.left <= 0) return false;
-  if (++w.g == a.h_kv) {
-    w.g = 0;
-    do { ++w.b; w.n = seq_units(a, w.b); } while (w.n == 0);
-  }
-  w.u = 0;
-  walk_piece(a, w);
-  return true;
+  return ++w.t < w.te || walk_pair<kTile>(a, w);
 }
 
 // the page of every 16-token group of the walk's tile (-1: no token of the piece in it)
@@ -191,7 +203,7 @@ __device__ __forceinline__ void fetch_pages(const Args& a, const Walk& w, int (&
   const int32_t* row = a.table + static_cast<int64_t>(w.b) * a.max_pages;
 #pragma unroll
   for (int i = 0; i < kTile / kUnit; ++i)
-    page[i] = w.u + i < w.ue ? __ldg(row + ((w.u + i) >> (a.page_shift - 4))) : -1;
+    page[i] = w.t * kTile + i * kUnit < w.tok_end ? __ldg(row + ((w.t * kTile + i * kUnit) >> a.page_shift)) : -1;
 }
 
 template <int D, bool F8>
@@ -200,15 +212,15 @@ __device__ __forceinline__ void issue_tile(const Args& a, const Walk& w, const i
   using C = Cfg<D, F8>;
   constexpr int NG = C::kTile / kUnit;   // 16-token groups
   constexpr int IPG = 8 / NG;            // instructions a group: 512 contiguous bytes each
-  const int tok0 = w.u * kUnit;
+  const int tok0 = w.t * C::kTile;
   const int nv = min(C::kTile, w.tok_end - tok0);
-  const int mask = (1 << (a.page_shift - 4)) - 1;
+  const int mask = (1 << a.page_shift) - 1;
   const int r0 = lane / C::CH, c = lane % C::CH;   // instruction i: tokens S i + r0
   int64_t at[NG];                        // first row of the group
   bool ok = nv == C::kTile;
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
-    at[i] = ((static_cast<int64_t>(page[i]) * a.h_kv + w.g) << a.page_shift) + (((w.u + i) & mask) << 4);
+    at[i] = ((static_cast<int64_t>(page[i]) * a.h_kv + w.g) << a.page_shift) + ((tok0 + i * kUnit) & mask);
     ok = ok && page[i] >= 0 && page[i] < a.n_pages;
   }
   if (ok) {
@@ -567,16 +579,16 @@ template <int D, bool F8, int NH>
 __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_constant__ Args a) {
   using C = Cfg<D, F8>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t chunk[32 * kWarps + 1];   // units (one kv head) before each thread's share of the sequences
+  __shared__ int64_t chunk[32 * kWarps + 1];   // cost before each thread's share of the sequences
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   dec::griddep_launch_dependents();
 
-  // units of all sequences
+  // cost of all sequences
   const int per = (a.batch + 32 * kWarps - 1) / (32 * kWarps);
   const int b_lo = min(a.batch, static_cast<int>(threadIdx.x) * per), b_hi = min(a.batch, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(a, b);
-  int64_t incl = mine;
+  int64_t incl = 0;
+  for (int b = b_lo; b < b_hi; ++b) incl += pair_cost(seq_tiles<C::kTile>(a, b));
+  incl *= a.h_kv;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -584,24 +596,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
   }
   if (lane == 31) chunk[warp] = incl;
   __syncthreads();
-  int64_t before = 0;
-  for (int w = 0; w < warp; ++w) before += chunk[w];
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t c = chunk[w];
+    if (w < warp) before += c;
+    total += c;
+  }
   __syncthreads();
   chunk[threadIdx.x + 1] = before + incl;
   if (threadIdx.x == 0) chunk[0] = 0;
   __syncthreads();
-  const int64_t units = chunk[32 * kWarps] * a.h_kv;
-  if (blockIdx.x == 0) {
-    int64_t at = chunk[threadIdx.x];
-    for (int b = b_lo; b < b_hi; ++b) {
-      a.prefix[b] = at;
-      at += seq_units(a, b);
-    }
-    if (threadIdx.x == 32 * kWarps - 1) a.prefix[a.batch] = chunk[32 * kWarps];
-  }
   // sequences with no keys: zeros and -inf
   for (int b = blockIdx.x * kWarps + warp; b < a.batch; b += a.ctas * kWarps) {
-    if (seq_units(a, b) > 0) continue;
+    if (seq_tiles<C::kTile>(a, b) > 0) continue;
     const int64_t row = static_cast<int64_t>(b) * a.h_kv * a.G;
     const int n = a.h_kv * a.G;
     for (int i = lane; i < n * D / 8; i += 32) {
@@ -614,126 +622,105 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     }
     if (a.lse)
       for (int i = lane; i < n; i += 32) a.lse[row + i] = -INFINITY;
+    if (a.by_pair)
+      for (int i = lane; i < a.h_kv; i += 32) a.desc[static_cast<int64_t>(b) * a.h_kv + i] = make_int2(0, 0);
   }
 
-  // this warp's range: consecutive ranges lie on different SMs
-  const int nw = static_cast<int>(min(units, static_cast<int64_t>(a.ctas) * kWarps));
+  // this warp's range; consecutive ranges lie on different SMs
   const int wk = warp * a.ctas + blockIdx.x;
-  if (wk >= nw) return;
-  const int64_t u0 = range_begin(units, wk, nw), u1 = range_begin(units, wk + 1, nw);
+  const int64_t share = div_pos(total + a.ctas * kWarps - 1, a.ctas * kWarps);
+  const int64_t x0 = min(total, share * wk), x1 = min(total, x0 + share);
+  int2 joins = make_int2(0, 0);
   Walk prod;
-  {
-    int lo = 0, hi = 32 * kWarps - 1;   // last share that begins at or before u0
+  bool more = x0 < x1;
+  if (more) {
+    int lo = 0, hi = 32 * kWarps - 1;   // last share of sequences that begins at or before x0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (chunk[mid] * a.h_kv <= u0) lo = mid; else hi = mid - 1;
+      if (chunk[mid] <= x0) lo = mid; else hi = mid - 1;
     }
-    int64_t r = u0 - chunk[lo] * a.h_kv;
+    int64_t r = x0 - chunk[lo];
+    int64_t cost;
     prod.b = lo * per;
-    for (;;) {
-      prod.n = seq_units(a, prod.b);
-      const int64_t all = static_cast<int64_t>(prod.n) * a.h_kv;
-      if (r < all) break;
-      r -= all;
-      ++prod.b;
+    for (;; ++prod.b) {
+      prod.n = seq_tiles<C::kTile>(a, prod.b);
+      cost = pair_cost(prod.n);
+      if (r < cost * a.h_kv) break;
+      r -= cost * a.h_kv;
     }
-    prod.g = static_cast<int>(r / prod.n);
-    prod.u = static_cast<int>(r - static_cast<int64_t>(prod.g) * prod.n);
-    prod.left = u1 - u0;
-    walk_piece(a, prod);
+    prod.g = static_cast<int>(div_pos(r, cost));
+    prod.left = x1 - x0;
+    more = walk_piece<C::kTile>(a, prod, static_cast<int>(r - prod.g * cost)) || walk_pair<C::kTile>(a, prod);
   }
   Walk cons = prod;
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
-  bool more = true;
   int page[C::kTile / kUnit];
-  fetch_pages<C::kTile>(a, prod, page);
-  auto produce = [&](int slot) {
+  if (more) fetch_pages<C::kTile>(a, prod, page);
+  State<D, F8, NH> st;
+  Query<D, F8, NH> q;
+  bool first = true, run = more;
+  int t0 = 0;
+  // iteration i copies tile i into its slot and attends to tile i - (kStages - 1)
+  for (int i = 0, slot = 0; run; ++i, slot = slot == kStages - 1 ? 0 : slot + 1) {
     if (more) {
       issue_tile<D, F8>(a, prod, page, ring + slot * C::kStage, lane);
       more = walk_next<C::kTile>(a, prod);
       if (more) fetch_pages<C::kTile>(a, prod, page);
     }
     cp_async_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) produce(s);
-  State<D, F8, NH> st;
-  Query<D, F8, NH> q;
-  bool first = true;
-  int piece_u = 0;
-  for (int slot = 0;; slot = slot == kStages - 1 ? 0 : slot + 1) {
-    cp_async_wait_n<kStages - 2>();
-    __syncwarp();
-    produce(slot == 0 ? kStages - 1 : slot - 1);
+    if (i < kStages - 1) continue;
     if (first) {
       load_query<D, F8, NH>(q, a.q + (static_cast<int64_t>(cons.b) * a.h_kv + cons.g) * a.G * D, lane, a.G,
                             a.scale_log2);
       state_clear(st);
-      piece_u = cons.u;
+      t0 = cons.t;
     }
-    attend_tile<D, F8, NH>(st, q, ring + slot * C::kStage, min(C::kTile, cons.tok_end - cons.u * kUnit), lane);
-    first = cons.u + C::kTile / kUnit >= cons.ue;
+    cp_async_wait_n<kStages - 1>();
+    __syncwarp();
+    attend_tile<D, F8, NH>(st, q, ring + (slot == kStages - 1 ? 0 : slot + 1) * C::kStage,
+                           min(C::kTile, cons.tok_end - cons.t * C::kTile), lane);
+    __syncwarp();
+    first = cons.t + 1 == cons.te;
     if (first) {
-      const bool from0 = piece_u == 0, to_end = cons.ue == cons.n;
       // a range has at most one piece begun in another range and one that goes on into the next
+      const bool from0 = t0 == 0, to_end = cons.te == cons.n;
       write_piece<D, F8, NH>(a, st, cons.b, cons.g, from0 && to_end ? -1 : 2 * wk + (from0 ? 1 : 0), lane);
+      const int pair = cons.b * a.h_kv + cons.g;
+      const int pieces = to_end ? 0 : 1 + static_cast<int>(div_pos(cons.n - cons.te + share - 1, share));
+      if (from0) {
+        if (a.by_pair) {
+          if (lane == 0) a.desc[pair] = make_int2(wk, pieces);
+        } else if (!to_end) {
+          joins = make_int2(pair, pieces);
+        }
+      }
     }
-    if (!walk_next<C::kTile>(a, cons)) break;
+    run = walk_next<C::kTile>(a, cons);
   }
+  if (!a.by_pair && lane == 0) a.desc[wk] = joins;
 }
 
 // Joins the partials of the (sequence, kv head) pairs that several ranges share:
 // out = sum_i 2^(lse_i - lse) o_i with lse = log2 sum_i 2^lse_i, pieces in
 // ascending order.  WPR warps take one query head's row.  Rows are enumerated
 // by pair, or, when there are more pairs than workers, by the worker whose
-// range ends inside the pair.
+// range the pair begins in.
 template <int D, int WPR>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int by_pair, int rows) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int rows) {
   constexpr int LPR = D / 4;            // lanes a piece
   constexpr int GR = 32 * WPR / LPR;    // pieces at a time
   __shared__ float4 acc[WPR > 1 ? GR : 1][LPR];
   const int row = blockIdx.x * (8 / WPR) + (threadIdx.x >> 5) / WPR;
+  const int at = row / a.G, h = row - at * a.G;
   dec::griddep_wait();
   if (row >= rows) return;
-  const int64_t total = a.prefix[a.batch];
-  const int64_t units = total * a.h_kv;
-  const int nw = static_cast<int>(min(units, static_cast<int64_t>(a.ctas) * kWarps));
-  const int h = row % a.G;
-  int b, g, wk;
-  int64_t s0, s1;
-  if (by_pair) {
-    b = row / a.G / a.h_kv;
-    g = row / a.G - b * a.h_kv;
-    const int64_t at = a.prefix[b], n = a.prefix[b + 1] - at;
-    if (n == 0) return;
-    s0 = at * a.h_kv + g * n;
-    s1 = s0 + n;
-    wk = static_cast<int>(s0 * nw / units);   // worker of unit s0
-    while (range_begin(units, wk, nw) > s0) --wk;
-    while (range_begin(units, wk + 1, nw) <= s0) ++wk;
-  } else {
-    wk = row / a.G;
-    if (wk >= nw - 1) return;
-    const int64_t u0 = range_begin(units, wk, nw), u1 = range_begin(units, wk + 1, nw);
-    int lo = 0, hi = a.batch - 1;             // the sequence of the range's last unit
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.prefix[mid] * a.h_kv <= u1 - 1) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
-    const int64_t first = a.prefix[b] * a.h_kv, n = a.prefix[b + 1] - a.prefix[b];
-    g = static_cast<int>((u1 - 1 - first) / n);
-    s0 = first + g * n;
-    s1 = s0 + n;
-    if (s0 < u0) return;                      // begun in an earlier range
-  }
-  if (s1 <= range_begin(units, wk + 1, nw)) return;   // one piece: written by its warp
-  int last = static_cast<int>((s1 - 1) * nw / units);
-  while (range_begin(units, last, nw) > s1 - 1) --last;
-  while (range_begin(units, last + 1, nw) <= s1 - 1) ++last;
+  const int2 d = a.desc[at];
+  const int np = d.y;
+  if (np == 0) return;                  // written by its warp
+  const int wk = a.by_pair ? d.x : at, pair = a.by_pair ? at : d.x;
   // piece i: the second slot of wk, then the first slot of wk + i
-  const int np = last - wk + 1;
   auto slot = [&](int i) { return static_cast<int64_t>(2 * (wk + i) + (i == 0 ? 1 : 0)) * a.G + h; };
+  const int c = threadIdx.x % LPR, r = (threadIdx.x % (32 * WPR)) / LPR;
   const int lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f;
   for (int i = lane; i < np; i += 32) m = fmaxf(m, a.part_lse[slot(i)]);
@@ -743,13 +730,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   for (int i = lane; i < np; i += 32) l += exp2f(a.part_lse[slot(i)] - mr);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int c = threadIdx.x % LPR, r = (threadIdx.x % (32 * WPR)) / LPR;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = r; i < np; i += GR) {
-    const float w = exp2f(a.part_lse[slot(i)] - mr) * inv;
     const float4 o = reinterpret_cast<const float4*>(a.part_o + slot(i) * D)[c];
+    const float w = exp2f(a.part_lse[slot(i)] - mr);
     s.x += w * o.x; s.y += w * o.y; s.z += w * o.z; s.w += w * o.w;
   }
   if (WPR > 1) {   // one row a CTA: no thread of it has returned
@@ -765,7 +750,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     s.z += __shfl_xor_sync(0xffffffffu, s.z, 16); s.w += __shfl_xor_sync(0xffffffffu, s.w, 16);
     if (r > 0) return;
   }
-  const int64_t orow = (static_cast<int64_t>(b) * a.h_kv + g) * a.G + h;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  s.x *= inv; s.y *= inv; s.z *= inv; s.w *= inv;
+  const int64_t orow = static_cast<int64_t>(pair) * a.G + h;
   if (a.out_f32) reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[c] = s;
   else
     reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[c] =
@@ -773,15 +760,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   if (a.lse && c == 0) a.lse[orow] = l == 0.f ? -INFINITY : m + log2f(l);
 }
 
-// workspace layout: prefix, partial log-sum-exps, partial rows
+// workspace layout: descriptors, partial log-sum-exps, partial rows
 struct Plan {
   size_t off_lse, off_o, bytes;
 };
-static Plan plan(int batch, int G, int d, int ctas) {
+static Plan plan(int G, int d, int ctas) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = static_cast<size_t>(2) * ctas * kWarps;
   Plan p;
-  p.off_lse = up((static_cast<size_t>(batch) + 1) * 8);
+  p.off_lse = up(slots / 2 * sizeof(int2));   // pairs (at most workers), or workers
   p.off_o = p.off_lse + up(slots * G * 4);
   p.bytes = p.off_o + up(slots * G * d * 4);
   return p;
@@ -809,9 +796,8 @@ static cudaError_t launch_heads(const Args& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  const int by_pair = pairs <= workers;
-  return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, a, by_pair, rows)
-              : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, by_pair, rows);
+  return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, a, rows)
+              : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, rows);
 }
 
 template <int D, bool F8>
@@ -822,9 +808,10 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
 }  // namespace pattn
 
 cudaError_t launch_paged_attn(pattn::Args a, int d, bool f8, void* workspace, cudaStream_t st) {
-  const pattn::Plan p = pattn::plan(a.batch, a.G, d, a.ctas);
+  const pattn::Plan p = pattn::plan(a.G, d, a.ctas);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.prefix = reinterpret_cast<int64_t*>(ws);
+  a.desc = reinterpret_cast<int2*>(ws);
+  a.by_pair = static_cast<int64_t>(a.batch) * a.h_kv <= static_cast<int64_t>(a.ctas) * pattn::kWarps;
   a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
   a.part_o = reinterpret_cast<float*>(ws + p.off_o);
   if (d == 128) return f8 ? pattn::launch<128, true>(a, st) : pattn::launch<128, false>(a, st);
