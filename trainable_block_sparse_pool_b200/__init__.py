@@ -380,30 +380,37 @@ def infllm2_decode_step(st: DecodeState, q: torch.Tensor, k_new: torch.Tensor, v
 
 
 # ------------------------------------------------------------------ rotary positions, paged cache
-def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> int:
-    """The data pointer of a contiguous tensor of this dtype and shape on `device`; raises otherwise."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise InfLLM2Error(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                           f"{t.dtype} {tuple(t.shape)} on {t.device}")
+def _expect(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
+    """The data pointer of a contiguous tensor of this dtype and shape on CUDA device `device` (-1: the CPU); raises
+    otherwise."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise InfLLM2Error(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on device {device}, "
+                           f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-class _on:
-    """The CUDA device of `t` as the current one for a call: a launch goes to the current device.  The library has no
-    CPU path, so a tensor elsewhere is refused."""
+def _cuda(t: torch.Tensor) -> int:
+    """The tensor's CUDA device; the library has no CPU path, so a tensor elsewhere is refused."""
+    i = t.get_device()
+    if i < 0:
+        raise InfLLM2Error(f"expected CUDA tensors, got one on {t.device}")
+    return i
 
-    def __init__(self, t: torch.Tensor):
-        if t.device.type != "cuda":
-            raise InfLLM2Error(f"expected CUDA tensors, got one on {t.device}")
-        self.to, self.back = t.device.index, torch.cuda.current_device()
 
-    def __enter__(self):
-        if self.to != self.back:
-            torch.cuda.set_device(self.to)
-
-    def __exit__(self, *exc):
-        if self.to != self.back:
-            torch.cuda.set_device(self.back)
+def _launch(name: str, device: int, stream, *args) -> None:
+    """One library call with `device` current (a launch goes to the current device), on `stream` or its current one."""
+    f = getattr(lib(), name)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)  # noqa: SLF001  (current_stream() without its wrapper)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, stream)
+    if rc != 0:
+        _check(name, rc)
 
 
 def make_rope(rot: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None, interleaved: bool = False,
@@ -425,18 +432,16 @@ def make_rope(rot: int, base: float = 10000.0, sections: Optional[Sequence[int]]
 
 
 def _rope(name: str, q, k, pos, rope, q_out, k_out, stream) -> None:
-    with _on(q):
-        if q.dim() != 3 or k.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float32):
-            raise InfLLM2Error(f"{name}: q and k are [total, heads, d] tensors of bf16 or fp32")
-        (total, h_q, d), h_kv, dt, dev = q.shape, k.shape[1], q.dtype, q.device
-        od = OUT_F32 if dt == torch.float32 else OUT_BF16
-        if pos.dim() == 1:
-            pos = pos[None]
-        rc = getattr(lib(), name)(_expect("q", q, dt, (total, h_q, d), dev), _expect("k", k, dt, (total, h_kv, d), dev),
-                                  od, _expect("pos", pos, torch.int32, (rope.n_axes, total), dev), total, h_q, h_kv, d,
-                                  ctypes.byref(rope), _expect("q_out", q_out, dt, q.shape, dev),
-                                  _expect("k_out", k_out, dt, k.shape, dev), _stream(stream))
-    _check(name, rc)
+    dev, dt, qs, ks = _cuda(q), q.dtype, q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or not (dt is torch.bfloat16 or dt is torch.float32):
+        raise InfLLM2Error(f"{name}: q and k are [total, heads, d] tensors of bf16 or fp32")
+    total, h_q, d = qs
+    h_kv, axes = ks[1], rope.n_axes
+    _launch(name, dev, stream, _expect("q", q, dt, qs, dev), _expect("k", k, dt, (total, h_kv, d), dev),
+            OUT_BF16 if dt is torch.bfloat16 else OUT_F32,
+            _expect("pos", pos, torch.int32, (total,) if axes == 1 and pos.dim() == 1 else (axes, total), dev),
+            total, h_q, h_kv, d, ctypes.byref(rope), _expect("q_out", q_out, dt, qs, dev),
+            _expect("k_out", k_out, dt, ks, dev))
 
 
 def infllm2_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, rope: RopeSpec, q_out: torch.Tensor,
@@ -457,7 +462,7 @@ def make_paged_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: 
                      k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None) -> PagedCache:
     """Paged cache over caller-owned device tensors: pages [n_pages, h_kv, page_size, d], bf16 or float8_e4m3fn (then
     with fp32 scales [n_pages, h_kv, page_size]), block_table int32 [batch, max_pages].  Keeps references."""
-    dev, dt, f8 = k_pages.device, k_pages.dtype, k_pages.dtype == torch.float8_e4m3fn
+    dev, dt, f8 = k_pages.get_device(), k_pages.dtype, k_pages.dtype == torch.float8_e4m3fn
     if k_pages.dim() != 4 or not (f8 or dt == torch.bfloat16) or block_table.dim() != 2:
         raise InfLLM2Error("pages are [n_pages, h_kv, page_size, d] tensors of bf16 or float8_e4m3fn, the table is "
                            "[batch, max_pages]")
@@ -473,7 +478,8 @@ def make_paged_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: 
     c.n_pages, c.h_kv, c.page_size, c.d = k_pages.shape
     c.batch, c.max_pages = block_table.shape
     c.dtype = KV_E4M3 if f8 else KV_BF16
-    c._keep = (k_pages, v_pages, block_table, k_scale, v_scale)  # noqa: SLF001
+    c._keep = (k_pages, v_pages, block_table, k_scale, v_scale)  # noqa: SLF001  (keeps the device buffers alive)
+    c._device = dev
     return c
 
 
@@ -481,30 +487,33 @@ def infllm2_paged_write(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, sta
                         cu_seqlens: Optional[torch.Tensor] = None, stream=None) -> None:
     """Writes packed rows K, V [total, h_kv, d] (bf16) into the pages: row i of sequence b goes to position
     start[b] + i.  cu_seqlens int32 [batch + 1]; None: one row a sequence."""
-    with _on(K):
-        shape, dev = (K.shape[0], cache.h_kv, cache.d), cache._keep[0].device  # noqa: SLF001
-        rc = lib().infllm2_paged_write(
-            ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev), _expect("V", V, torch.bfloat16, shape, dev),
-            _expect("start", start, torch.int32, (cache.batch,), dev),
-            None if cu_seqlens is None else _expect("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), dev),
-            K.shape[0], _stream(stream))
-    _check("infllm2_paged_write", rc)
+    _cuda(K)
+    dev, batch, total = cache._device, cache.batch, K.shape[0]  # noqa: SLF001
+    shape = (total, cache.h_kv, cache.d)
+    _launch("infllm2_paged_write", dev, stream, ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev),
+            _expect("V", V, torch.bfloat16, shape, dev), _expect("start", start, torch.int32, (batch,), dev),
+            None if cu_seqlens is None else _expect("cu_seqlens", cu_seqlens, torch.int32, (batch + 1,), dev), total)
 
 
 def infllm2_paged_read(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, cu_seqlens: torch.Tensor,
                        stream=None) -> None:
     """Reads positions 0 .. len-1 of every sequence into the packed rows of K, V [total, h_kv, d] (bf16)."""
-    with _on(K):
-        shape, dev = (K.shape[0], cache.h_kv, cache.d), cache._keep[0].device  # noqa: SLF001
-        rc = lib().infllm2_paged_read(
-            ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev), _expect("V", V, torch.bfloat16, shape, dev),
-            _expect("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), dev), K.shape[0], _stream(stream))
-    _check("infllm2_paged_read", rc)
+    _cuda(K)
+    dev, total = cache._device, K.shape[0]  # noqa: SLF001
+    shape = (total, cache.h_kv, cache.d)
+    _launch("infllm2_paged_read", dev, stream, ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev),
+            _expect("V", V, torch.bfloat16, shape, dev),
+            _expect("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), dev), total)
 
 
 def infllm2_paged_workspace_bytes(cache: PagedCache, h_q: int) -> int:
-    with _on(cache._keep[0]):  # noqa: SLF001
+    if cache._device < 0:  # noqa: SLF001
+        raise InfLLM2Error("the cache's tensors are not on a CUDA device")
+    with torch.cuda.device(cache._device):  # noqa: SLF001
         return int(lib().infllm2_paged_workspace_bytes(ctypes.byref(cache), h_q))
+
+
+_DEFAULTS: Optional[Params] = None
 
 
 def infllm2_paged_decode_attn(cache: PagedCache, q: torch.Tensor, seq_len: torch.Tensor, out: torch.Tensor,
@@ -512,17 +521,20 @@ def infllm2_paged_decode_attn(cache: PagedCache, q: torch.Tensor, seq_len: torch
                               params: Optional[Params] = None, stream=None) -> None:
     """Attention of one token a sequence, q [batch, h_q, d] (bf16), over the first seq_len[b] positions of its pages
     (its own row among them) into out [batch, h_q, d] (bf16 or fp32) and, if given, lse fp32 [batch, h_q]."""
-    with _on(q):
-        dev, batch = cache._keep[0].device, cache.batch  # noqa: SLF001
-        if q.dim() != 3 or out.dtype not in (torch.bfloat16, torch.float32):
-            raise InfLLM2Error("q is [batch, h_q, d], out bf16 or fp32")
-        h_q = q.shape[1]
-        shape = (batch, h_q, cache.d)
-        rc = lib().infllm2_paged_decode_attn(
-            ctypes.byref(cache), _expect("q", q, torch.bfloat16, shape, dev), h_q,
-            _expect("seq_len", seq_len, torch.int32, (batch,), dev), _expect("out", out, out.dtype, shape, dev),
-            OUT_F32 if out.dtype == torch.float32 else OUT_BF16,
+    global _DEFAULTS
+    if params is None:
+        if _DEFAULTS is None:
+            _DEFAULTS = default_params()
+        params = _DEFAULTS
+    _cuda(q)
+    dev, batch, od = cache._device, cache.batch, out.dtype  # noqa: SLF001
+    if q.dim() != 3 or not (od is torch.bfloat16 or od is torch.float32):
+        raise InfLLM2Error("q is [batch, h_q, d], out bf16 or fp32")
+    h_q = q.shape[1]
+    shape = (batch, h_q, cache.d)
+    _launch("infllm2_paged_decode_attn", dev, stream, ctypes.byref(cache), _expect("q", q, torch.bfloat16, shape, dev),
+            h_q, _expect("seq_len", seq_len, torch.int32, (batch,), dev), _expect("out", out, od, shape, dev),
+            OUT_BF16 if od is torch.bfloat16 else OUT_F32,
             None if lse is None else _expect("lse", lse, torch.float32, (batch, h_q), dev),
-            _expect("workspace", workspace, workspace.dtype, workspace.shape, dev),
-            workspace.numel() * workspace.element_size(), ctypes.byref(params or default_params()), _stream(stream))
-    _check("infllm2_paged_decode_attn", rc)
+            _expect("workspace", workspace, workspace.dtype, workspace.shape, dev), workspace.nbytes,
+            ctypes.byref(params))

@@ -39,8 +39,6 @@ namespace pattn {
 
 using dec::cp_async_commit;
 using dec::cp_async_wait_n;
-using dec::ldsm_x4_t;
-using dec::mma16816;
 
 #ifndef INFLLM2_PATTN_WARPS
 #define INFLLM2_PATTN_WARPS 8
@@ -54,12 +52,24 @@ constexpr int kUnit = 16;           // tokens; every page size is a multiple of 
 constexpr float kMargin = 4.f;      // the reference maximum is raised only past this many log2 units
 constexpr int kHalf = 4096;         // bytes of K, and of V, in a stage
 
-__device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// The products, the transposed loads and movmatrix are plain (not volatile) asm, so
+// the compiler may interleave the chains of a tile; tile_pin keeps them
+// between the wait for a tile and the reuse of its slot.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr));
 }
 // `bytes` (0 .. 16) from src, zeros after them
 __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, int bytes) {
@@ -70,18 +80,18 @@ __device__ __forceinline__ void cp_async16_full(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  asm("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  asm("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
 // transpose of an 8x8 matrix of 16-bit elements held two a lane
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -363,14 +373,14 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
                                  paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w0[i] >> 16)),
                                  paged::e4m3x2_to_f16x2(static_cast<uint16_t>(w1[i] >> 16))};
 #pragma unroll
-          for (int nh = 0; nh < NH; ++nh) mma16816_f16(z[m][nh], f, q.b[nh][4 * j + i][0], q.b[nh][4 * j + i][1]);
+          for (int nh = 0; nh < NH; ++nh) mma<true>(z[m][nh], f, q.b[nh][4 * j + i][0], q.b[nh][4 * j + i][1]);
         }
       } else {
         const uint32_t f0[4] = {k0.x, k1.x, k0.y, k1.y}, f1[4] = {k0.z, k1.z, k0.w, k1.w};
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
-          mma16816(z[m][nh], f0, q.b[nh][2 * j][0], q.b[nh][2 * j][1]);
-          mma16816(z[m][nh], f1, q.b[nh][2 * j + 1][0], q.b[nh][2 * j + 1][1]);
+          mma<false>(z[m][nh], f0, q.b[nh][2 * j][0], q.b[nh][2 * j][1]);
+          mma<false>(z[m][nh], f1, q.b[nh][2 * j + 1][0], q.b[nh][2 * j + 1][1]);
         }
       }
     }
@@ -507,7 +517,7 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
                                  paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi)),
                                  paged::e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16))};
 #pragma unroll
-          for (int nh = 0; nh < NH; ++nh) mma16816_f16(st.o[nh][2 * j + e], f, p[m][nh][0], p[m][nh][1]);
+          for (int nh = 0; nh < NH; ++nh) mma<true>(st.o[nh][2 * j + e], f, p[m][nh][0], p[m][nh][1]);
         }
     } else {
       // four 8x8 matrices: columns 0-7 and 8-15 of the tile, rows 0-7, then rows 8-15 of the step
@@ -517,9 +527,21 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
         uint32_t f[4];
         ldsm_x4_t(f, vb + piece_at<C::CH, C::S, F8>(lane & 7, 2 * m + (i >> 1), 2 * j + (i & 1)));
 #pragma unroll
-        for (int nh = 0; nh < NH; ++nh) mma16816(st.o[nh][j], f, p[m][nh][0], p[m][nh][1]);
+        for (int nh = 0; nh < NH; ++nh) mma<false>(st.o[nh][j], f, p[m][nh][0], p[m][nh][1]);
       }
     }
+  }
+}
+
+// Nothing that reads the tile moves past this point: its results are needed here.
+template <int D, bool F8, int NH>
+__device__ __forceinline__ void tile_pin(State<D, F8, NH>& st) {
+#pragma unroll
+  for (int nh = 0; nh < NH; ++nh) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      asm volatile("" : "+f"(st.o[nh][i][0]), "+f"(st.o[nh][i][1]), "+f"(st.o[nh][i][2]), "+f"(st.o[nh][i][3])::"memory");
+    asm volatile("" : "+f"(st.l[nh][0]), "+f"(st.l[nh][1])::"memory");
   }
 }
 
@@ -634,11 +656,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
   Walk prod;
   bool more = x0 < x1;
   if (more) {
-    int lo = 0, hi = 32 * kWarps - 1;   // last share of sequences that begins at or before x0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (chunk[mid] <= x0) lo = mid; else hi = mid - 1;
-    }
+    // the last share of sequences that begins at or before x0: among every kWarps-th, then next to it
+    int lo = 31 - __clz(__ballot_sync(0xffffffffu, chunk[lane * kWarps] <= x0));
+    lo *= kWarps;
+    lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < kWarps && chunk[lo + lane] <= x0));
     int64_t r = x0 - chunk[lo];
     int64_t cost;
     prod.b = lo * per;
@@ -677,8 +698,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     }
     cp_async_wait_n<kStages - 1>();
     __syncwarp();
-    attend_tile<D, F8, NH>(st, q, ring + (slot == kStages - 1 ? 0 : slot + 1) * C::kStage,
-                           min(C::kTile, cons.tok_end - cons.t * C::kTile), lane);
+    uint32_t stage = ring + (slot == kStages - 1 ? 0 : slot + 1) * C::kStage;
+    asm volatile("" : "+r"(stage)::"memory");   // the tile's loads stay behind the wait
+    attend_tile<D, F8, NH>(st, q, stage, min(C::kTile, cons.tok_end - cons.t * C::kTile), lane);
+    tile_pin(st);
     __syncwarp();
     first = cons.t + 1 == cons.te;
     if (first) {
@@ -710,6 +733,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   constexpr int LPR = D / 4;            // lanes a piece
   constexpr int GR = 32 * WPR / LPR;    // pieces at a time
   __shared__ float4 acc[WPR > 1 ? GR : 1][LPR];
+  __shared__ float2 stat[WPR > 1 ? GR : 1];
   const int row = blockIdx.x * (8 / WPR) + (threadIdx.x >> 5) / WPR;
   const int at = row / a.G, h = row - at * a.G;
   dec::griddep_wait();
@@ -721,34 +745,60 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   // piece i: the second slot of wk, then the first slot of wk + i
   auto slot = [&](int i) { return static_cast<int64_t>(2 * (wk + i) + (i == 0 ? 1 : 0)) * a.G + h; };
   const int c = threadIdx.x % LPR, r = (threadIdx.x % (32 * WPR)) / LPR;
-  const int lane = threadIdx.x & 31;
+  // this thread's pieces with a running maximum, eight loads in flight
   float m = -INFINITY, l = 0.f;
-  for (int i = lane; i < np; i += 32) m = fmaxf(m, a.part_lse[slot(i)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float mr = m == -INFINITY ? 0.f : m;
-  for (int i = lane; i < np; i += 32) l += exp2f(a.part_lse[slot(i)] - mr);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = r; i < np; i += GR) {
-    const float4 o = reinterpret_cast<const float4*>(a.part_o + slot(i) * D)[c];
-    const float w = exp2f(a.part_lse[slot(i)] - mr);
-    s.x += w * o.x; s.y += w * o.y; s.z += w * o.z; s.w += w * o.w;
+  for (int i0 = r; i0 < np; i0 += 8 * GR) {
+    float4 o[8];
+    float x[8];
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * GR;
+      x[j] = i < np ? a.part_lse[slot(i)] : -INFINITY;
+      o[j] = i < np ? reinterpret_cast<const float4*>(a.part_o + slot(i) * D)[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = exp2f(m - ref);
+    l *= f; s.x *= f; s.y *= f; s.z *= f; s.w *= f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float w = exp2f(x[j] - ref);
+      l += w;
+      s.x += w * o[j].x; s.y += w * o[j].y; s.z += w * o[j].z; s.w += w * o[j].w;
+    }
+    m = top;
   }
+  // the groups' sums
   if (WPR > 1) {   // one row a CTA: no thread of it has returned
     acc[r][c] = s;
+    if (c == 0) stat[r] = make_float2(m, l);
     __syncthreads();
     if (r > 0) return;
+    float top = m;
+#pragma unroll
+    for (int i = 1; i < GR; ++i) top = fmaxf(top, stat[i].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = exp2f(m - ref);
+    l *= f; s.x *= f; s.y *= f; s.z *= f; s.w *= f;
 #pragma unroll
     for (int i = 1; i < GR; ++i) {
-      s.x += acc[i][c].x; s.y += acc[i][c].y; s.z += acc[i][c].z; s.w += acc[i][c].w;
+      const float w = exp2f(stat[i].x - ref);
+      l += w * stat[i].y;
+      s.x += w * acc[i][c].x; s.y += w * acc[i][c].y; s.z += w * acc[i][c].z; s.w += w * acc[i][c].w;
     }
+    m = top;
   } else if (GR > 1) {
+    const float top = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    const float f = exp2f(m - (top == -INFINITY ? 0.f : top));
+    l *= f; s.x *= f; s.y *= f; s.z *= f; s.w *= f;
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
     s.x += __shfl_xor_sync(0xffffffffu, s.x, 16); s.y += __shfl_xor_sync(0xffffffffu, s.y, 16);
     s.z += __shfl_xor_sync(0xffffffffu, s.z, 16); s.w += __shfl_xor_sync(0xffffffffu, s.w, 16);
     if (r > 0) return;
+    m = top;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   s.x *= inv; s.y *= inv; s.z *= inv; s.w *= inv;
