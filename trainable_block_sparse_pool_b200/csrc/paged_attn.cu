@@ -14,11 +14,12 @@
 // Split.  Lengths are known on the device only, so the grid is fixed (one CTA
 // an SM) and every warp works alone: the tiles of all (sequence, kv head) pairs,
 // in order, each pair with one more for its start and end, are cut into equal
-// ranges, one a warp, whatever the lengths.  A piece of a pair that begins and
-// ends within one range is written out by its warp; the others leave a
-// normalised partial and its log-sum-exp in the workspace, and a second kernel
-// (programmatic dependent launch) joins them in ascending order.  Nothing waits
-// on another CTA.
+// ranges, one a warp, whatever the lengths.  A warp's last piece of a pair meets
+// those of the CTA's next warps in shared memory when they belong to the same
+// pair; a pair that then lies within one CTA's run of warps is written out, and
+// the others leave normalised partials and their log-sum-exps in the workspace,
+// at most one a CTA and one more, which a second kernel (programmatic dependent
+// launch) joins in ascending order.  Nothing waits on another CTA.
 //
 // A warp streams tiles of 8 KB (K and V of 16, 32 or 64 tokens) through its own
 // kStages-deep cp.async ring, the page numbers of a tile fetched one tile ahead
@@ -88,6 +89,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+// (volatile: issued in program order, all before their first use)
+__device__ __forceinline__ void ld_part(float& v, const float* p) {
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+}
+__device__ __forceinline__ void ld_part(float4& v, const float* p) {
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+}
 // transpose of an 8x8 matrix of 16-bit elements held two a lane
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
@@ -115,7 +123,7 @@ struct Args {
   const __nv_bfloat16* q;
   void* out;
   float* lse;             // [batch, h_q] or null
-  int2* desc;             // workspace: what to join; by pair: (first worker, pieces), by worker: (pair, pieces)
+  int4* desc;             // workspace: what to join; by pair (first worker, CTAs, last worker or -1), by worker (pair, ...)
   float* part_o;          // workspace: [2 * workers][G][D]
   float* part_lse;        // workspace: [2 * workers][G]
   int32_t by_pair;        // at most as many pairs as workers
@@ -545,9 +553,11 @@ __device__ __forceinline__ void tile_pin(State<D, F8, NH>& st) {
   }
 }
 
-// The G heads' normalised rows and log-sum-exps: to out and lse (slot < 0), or to partial `slot`.
+// The G heads' normalised rows and log-sum-exps: to `mine` (G rows, then G log-sum-exps); with mine null to the
+// pair's rows of the output (`out`) or to partial `slot`.
 template <int D, bool F8, int NH>
-__device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st, int b, int g, int64_t slot, int lane) {
+__device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st, float* mine, bool out, int pair,
+                                            int64_t slot, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh)
@@ -563,15 +573,11 @@ __device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st,
       float inv = l == 0.f ? 0.f : 1.f / l;
       if (F8) inv *= __uint_as_float(static_cast<uint32_t>(st.e_r - 11) << 23);
       const float lse = l == 0.f ? -INFINITY : st.m[nh][e] + log2f(l);
-      const int64_t row = (static_cast<int64_t>(b) * a.h_kv + g) * a.G + h;
-      float* po = nullptr;
-      if (slot >= 0) {
-        po = a.part_o + (slot * a.G + h) * D;
-        if (gid == 0) a.part_lse[slot * a.G + h] = lse;
-      } else {
-        if (a.out_f32) po = static_cast<float*>(a.out) + row * D;
-        if (a.lse && gid == 0) a.lse[row] = lse;
-      }
+      const int64_t row = (out ? pair : slot) * a.G + h;
+      float* po = mine ? mine + h * D : (!out ? a.part_o : a.out_f32 ? static_cast<float*>(a.out) : nullptr) + row * D;
+      float* pl = mine ? mine + a.G * D + h : (out ? a.lse : a.part_lse) + row;
+      const bool b16 = !mine && out && !a.out_f32;
+      if (gid == 0 && (mine || !out || a.lse)) *pl = lse;
       __nv_bfloat16* pb = static_cast<__nv_bfloat16*>(a.out) + row * D;
       if (F8) {
         // columns D/8 gid .. D/8 (gid + 1)
@@ -580,7 +586,7 @@ __device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st,
           const float v0 = st.o[nh][i][e] * inv, v1 = st.o[nh][i][2 + e] * inv;
           const float v2 = st.o[nh][i + 1][e] * inv, v3 = st.o[nh][i + 1][2 + e] * inv;
           const int d = D / 8 * gid + 2 * i;
-          if (po) *reinterpret_cast<float4*>(po + d) = make_float4(v0, v1, v2, v3);
+          if (!b16) *reinterpret_cast<float4*>(po + d) = make_float4(v0, v1, v2, v3);
           else *reinterpret_cast<uint2*>(pb + d) = make_uint2(pack_bf16(v0, v1), pack_bf16(v2, v3));
         }
       } else {
@@ -590,7 +596,7 @@ __device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st,
           for (int r = 0; r < 2; ++r) {
             const float v = st.o[nh][i][2 * r + e] * inv;
             const int d = 16 * i + 8 * r + gid;
-            if (po) po[d] = v;
+            if (!b16) po[d] = v;
             else pb[d] = __float2bfloat16_rn(v);
           }
       }
@@ -602,6 +608,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
   using C = Cfg<D, F8>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t chunk[32 * kWarps + 1];   // cost before each thread's share of the sequences
+  __shared__ int4 info[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   dec::griddep_launch_dependents();
 
@@ -645,14 +652,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     if (a.lse)
       for (int i = lane; i < n; i += 32) a.lse[row + i] = -INFINITY;
     if (a.by_pair)
-      for (int i = lane; i < a.h_kv; i += 32) a.desc[static_cast<int64_t>(b) * a.h_kv + i] = make_int2(0, 0);
+      for (int i = lane; i < a.h_kv; i += 32) a.desc[static_cast<int64_t>(b) * a.h_kv + i] = make_int4(0, 0, -1, 0);
   }
 
-  // this warp's range; consecutive ranges lie on different SMs
-  const int wk = warp * a.ctas + blockIdx.x;
+  // this warp's range
+  const int wk = blockIdx.x * kWarps + warp;
   const int64_t share = div_pos(total + a.ctas * kWarps - 1, a.ctas * kWarps);
   const int64_t x0 = min(total, share * wk), x1 = min(total, x0 + share);
-  int2 joins = make_int2(0, 0);
   Walk prod;
   bool more = x0 < x1;
   if (more) {
@@ -680,7 +686,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
   State<D, F8, NH> st;
   Query<D, F8, NH> q;
   bool first = true, run = more;
-  int t0 = 0;
+  int t0 = 0, pieces = 0, rest = 0;
+  int4 last = make_int4(-1, 0, 0, 0);   // the last piece: its pair, from the start?, to the end?, the only one?
   // iteration i copies tile i into its slot and attends to tile i - (kStages - 1)
   for (int i = 0, slot = 0; run; ++i, slot = slot == kStages - 1 ? 0 : slot + 1) {
     if (more) {
@@ -705,22 +712,87 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     __syncwarp();
     first = cons.t + 1 == cons.te;
     if (first) {
-      // a range has at most one piece begun in another range and one that goes on into the next
-      const bool from0 = t0 == 0, to_end = cons.te == cons.n;
-      write_piece<D, F8, NH>(a, st, cons.b, cons.g, from0 && to_end ? -1 : 2 * wk + (from0 ? 1 : 0), lane);
       const int pair = cons.b * a.h_kv + cons.g;
-      const int pieces = to_end ? 0 : 1 + static_cast<int>(div_pos(cons.n - cons.te + share - 1, share));
-      if (from0) {
-        if (a.by_pair) {
-          if (lane == 0) a.desc[pair] = make_int2(wk, pieces);
-        } else if (!to_end) {
-          joins = make_int2(pair, pieces);
-        }
-      }
+      const bool from0 = t0 == 0;
+      last = make_int4(pair, from0, cons.te == cons.n, pieces++ == 0);
+      rest = cons.n - cons.te;
+      // the range's last piece waits in this warp's share of the ring; an earlier one ends its pair
+      const bool keep = cons.left <= 1;   // (what is left is no other pair's tile)
+      write_piece<D, F8, NH>(a, st, keep ? reinterpret_cast<float*>(smem + warp * kStages * C::kStage) : nullptr,
+                             from0, pair, 2 * static_cast<int64_t>(wk), lane);
+      if (!keep && from0 && a.by_pair && lane == 0) a.desc[pair] = make_int4(0, 0, -1, 0);
     }
     run = walk_next<C::kTile>(a, cons);
   }
-  if (!a.by_pair && lane == 0) a.desc[wk] = joins;
+  cp_async_wait_n<0>();
+  if (lane == 0) info[warp] = last;
+  __syncthreads();
+  // Runs of warps whose last pieces are of one pair: the CTA's threads share a
+  // run's rows, four columns a thread.
+  constexpr int kWarpFloats = kStages * C::kStage / 4;
+  for (int w0 = 0, w1; w0 < kWarps; w0 = w1 + 1) {
+    const int4 head = info[w0];
+    w1 = w0;
+    if (head.x < 0) continue;
+    int4 tail = head;
+    while (w1 < kWarps - 1) {
+      const int4 next = info[w1 + 1];
+      if (next.x != head.x || !next.w) break;
+      tail = next;
+      ++w1;
+    }
+    const bool out = head.y && tail.z;
+    const float* part = reinterpret_cast<const float*>(smem) + w0 * kWarpFloats;
+    const int len = w1 - w0 + 1;
+    const int64_t row0 = (out ? head.x : 2 * static_cast<int64_t>(blockIdx.x * kWarps + w0) + (head.y ? 1 : 0)) * a.G;
+    for (int i = threadIdx.x; i < a.G * (D / 4); i += 32 * kWarps) {
+      const int h = i / (D / 4);
+      float4 o = reinterpret_cast<const float4*>(part)[i];
+      float lse = part[a.G * D + h];
+      if (len > 1) {
+        float x[kWarps], m = lse;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          x[w] = part[min(w, len - 1) * kWarpFloats + a.G * D + h];
+          m = fmaxf(m, x[w]);
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float l = ex2(lse - ref);
+        o.x *= l; o.y *= l; o.z *= l; o.w *= l;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w)
+          if (w < len) {
+            const float f = ex2(x[w] - ref);
+            const float4 v = reinterpret_cast<const float4*>(part + w * kWarpFloats)[i];
+            l += f;
+            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+          }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+        lse = l == 0.f ? -INFINITY : m + log2f(l);
+      }
+      const int64_t at = row0 * (D / 4) + i;
+      if (!out) reinterpret_cast<float4*>(a.part_o)[at] = o;
+      else if (a.out_f32) reinterpret_cast<float4*>(a.out)[at] = o;
+      else reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+      if (i % (D / 4) == 0 && (!out || a.lse)) (out ? a.lse : a.part_lse)[row0 + h] = lse;
+    }
+    if (warp == w0 && lane == 0) {   // its first warp describes a run
+      int4 joins = make_int4(a.by_pair ? wk : head.x, 0, -1, 0);
+      if (head.y && !tail.z) {
+        // the pair's end, its last worker, and whether that one goes on to another pair's tiles
+        const int64_t end = x1 + rest;
+        const int wl = static_cast<int>(div_pos(end - 1, share)), c1 = wl / kWarps;
+        const bool on = min(total, (wl + 1) * share) - end >= 2;
+        joins.y = c1 - static_cast<int>(blockIdx.x) + 1;
+        if (on && wl > max(wk, c1 * kWarps)) joins.z = wl;
+      }
+      if (!a.by_pair) a.desc[wk] = joins;
+      else if (head.y) a.desc[head.x] = joins;
+    }
+    if (!a.by_pair && lane == 0 && warp > w0 && warp <= w1) a.desc[wk] = make_int4(0, 0, -1, 0);
+  }
+  if (!a.by_pair && last.x < 0 && lane == 0) a.desc[wk] = make_int4(0, 0, -1, 0);
 }
 
 // Joins the partials of the (sequence, kv head) pairs that several ranges share:
@@ -732,18 +804,24 @@ template <int D, int WPR>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int rows) {
   constexpr int LPR = D / 4;            // lanes a piece
   constexpr int GR = 32 * WPR / LPR;    // pieces at a time
-  __shared__ float4 acc[WPR > 1 ? GR : 1][LPR];
-  __shared__ float2 stat[WPR > 1 ? GR : 1];
-  const int row = blockIdx.x * (8 / WPR) + (threadIdx.x >> 5) / WPR;
+  constexpr int RPC = 8 / WPR;          // rows a CTA
+  __shared__ float4 acc_s[RPC][WPR > 1 ? GR : 1][LPR];
+  __shared__ float2 stat_s[RPC][WPR > 1 ? GR : 1];
+  auto& acc = acc_s[(threadIdx.x >> 5) / WPR];
+  auto& stat = stat_s[(threadIdx.x >> 5) / WPR];
+  const int row = blockIdx.x * RPC + (threadIdx.x >> 5) / WPR;
   const int at = row / a.G, h = row - at * a.G;
   dec::griddep_wait();
   if (row >= rows) return;
-  const int2 d = a.desc[at];
-  const int np = d.y;
-  if (np == 0) return;                  // written by its warp
+  const int4 d = a.desc[at];
+  if (d.y == 0) return;                 // written by its warps
+  const int np = d.y + (d.z >= 0 ? 1 : 0);
   const int wk = a.by_pair ? d.x : at, pair = a.by_pair ? at : d.x;
-  // piece i: the second slot of wk, then the first slot of wk + i
-  auto slot = [&](int i) { return static_cast<int64_t>(2 * (wk + i) + (i == 0 ? 1 : 0)) * a.G + h; };
+  // the second slot of wk, the first slots of the next CTAs' first workers, and that of worker d.z
+  auto slot = [&](int i) {
+    const int w = i == 0 ? wk : i < d.y ? (wk / kWarps + i) * kWarps : d.z;
+    return static_cast<int64_t>(2 * w + (i == 0 ? 1 : 0)) * a.G + h;
+  };
   const int c = threadIdx.x % LPR, r = (threadIdx.x % (32 * WPR)) / LPR;
   // this thread's pieces with a running maximum, eight loads in flight
   float m = -INFINITY, l = 0.f;
@@ -753,18 +831,22 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     float x[8];
     float top = m;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j * GR;
-      x[j] = i < np ? a.part_lse[slot(i)] : -INFINITY;
-      o[j] = i < np ? reinterpret_cast<const float4*>(a.part_o + slot(i) * D)[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < 8; ++j) {   // past the last piece: that piece again, without weight
+      const int64_t at = slot(min(i0 + j * GR, np - 1));
+      ld_part(x[j], a.part_lse + at);
+      ld_part(o[j], a.part_o + at * D + 4 * c);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]);
+    for (int j = 0; j < 8; ++j) {
+      if (i0 + j * GR >= np) x[j] = -INFINITY;
+      top = fmaxf(top, x[j]);
+    }
     const float ref = top == -INFINITY ? 0.f : top;
     const float f = exp2f(m - ref);
     l *= f; s.x *= f; s.y *= f; s.z *= f; s.w *= f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      if (i0 + j * GR >= np) break;
       const float w = exp2f(x[j] - ref);
       l += w;
       s.x += w * o[j].x; s.y += w * o[j].y; s.z += w * o[j].z; s.w += w * o[j].w;
@@ -772,10 +854,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     m = top;
   }
   // the groups' sums
-  if (WPR > 1) {   // one row a CTA: no thread of it has returned
+  if (WPR > 1) {   // all warps of a row come here or none
     acc[r][c] = s;
     if (c == 0) stat[r] = make_float2(m, l);
-    __syncthreads();
+    if (WPR == 8) __syncthreads();
+    else named_bar_sync(1 + (threadIdx.x >> 5) / WPR, 32 * WPR);
     if (r > 0) return;
     float top = m;
 #pragma unroll
@@ -818,7 +901,7 @@ static Plan plan(int G, int d, int ctas) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = static_cast<size_t>(2) * ctas * kWarps;
   Plan p;
-  p.off_lse = up(slots / 2 * sizeof(int2));   // pairs (at most workers), or workers
+  p.off_lse = up(slots / 2 * sizeof(int4));   // pairs (at most workers), or workers
   p.off_o = p.off_lse + up(slots * G * 4);
   p.bytes = p.off_o + up(slots * G * d * 4);
   return p;
@@ -835,19 +918,26 @@ static cudaError_t launch_heads(const Args& a, cudaStream_t st) {
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  // Few pairs have many pieces each: a CTA a row.  More pairs than SMs: about
-  // kWarps pieces or fewer each, a warp a row.
+  // A warp joins 8 pieces (16 for d = 64) at a time: one warp a row where pairs have
+  // few (at most CTAs / pairs and two, on average), else four or a CTA, so
+  // that rows of a few times the average take one round.
   const int64_t pairs = static_cast<int64_t>(a.batch) * a.h_kv;
   const int64_t workers = static_cast<int64_t>(a.ctas) * kWarps;
   const int rows = static_cast<int>(std::min(pairs, workers) * a.G);
-  const bool wide = pairs <= a.ctas;
-  cfg.gridDim = dim3(wide ? rows : (rows + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, a, rows)
-              : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, rows);
+  if (pairs * 8 < a.ctas) {
+    cfg.gridDim = dim3(rows);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, a, rows);
+  }
+  if (pairs < a.ctas) {
+    cfg.gridDim = dim3((rows + 1) / 2);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, 4>, a, rows);
+  }
+  cfg.gridDim = dim3((rows + 7) / 8);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, rows);
 }
 
 template <int D, bool F8>
@@ -860,7 +950,7 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
 cudaError_t launch_paged_attn(pattn::Args a, int d, bool f8, void* workspace, cudaStream_t st) {
   const pattn::Plan p = pattn::plan(a.G, d, a.ctas);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.desc = reinterpret_cast<int2*>(ws);
+  a.desc = reinterpret_cast<int4*>(ws);
   a.by_pair = static_cast<int64_t>(a.batch) * a.h_kv <= static_cast<int64_t>(a.ctas) * pattn::kWarps;
   a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
   a.part_o = reinterpret_cast<float*>(ws + p.off_o);
