@@ -12,9 +12,9 @@
 // series (truncation below 2e-9), and turned by the quarter.
 //
 // HBM-bound: each element is read once and written once.  A thread holds
-// eight pairs (16 elements) of a token and walks several heads of it with the
-// same sines and cosines in registers, its loads of all heads in flight
-// before the angles are computed.
+// eight pairs of a token (16-byte vectors that neighbouring threads hold side by
+// side) and walks several heads of it with the same sines and cosines in
+// registers, its loads of all heads in flight before the angles are computed.
 #include "sm100.cuh"
 
 namespace infllm2 {
@@ -44,6 +44,12 @@ __device__ __forceinline__ uint32_t angle(int32_t pos, uint64_t turns) {
   return static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns) >> 32);
 }
 
+__device__ __forceinline__ void turn_pair(float& u, float& v, float c, float s) {
+  const float x = u;
+  u = x * c - v * s;
+  v = v * c + x * s;
+}
+
 struct Args {
   const void* q;
   const void* k;
@@ -55,10 +61,12 @@ struct Args {
   uint64_t turns[INFLLM2_ROPE_MAX_PAIRS];
 };
 
+// 16 bytes of elements
 template <typename T>
-struct Vec8;   // eight elements, loaded and stored as 16-byte pieces
+struct Vec;
 template <>
-struct Vec8<__nv_bfloat16> {
+struct Vec<__nv_bfloat16> {
+  static constexpr int W = 8;
   uint4 r;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -81,31 +89,22 @@ struct Vec8<__nv_bfloat16> {
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = r; }
 };
 template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
-    a = make_float4(x[0], x[1], x[2], x[3]);
-    b = make_float4(x[4], x[5], x[6], x[7]);
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
+struct Vec<float> {
+  static constexpr int W = 4;
+  float4 r;
+  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w; }
+  __device__ __forceinline__ void set(const float (&x)[4]) { r = make_float4(x[0], x[1], x[2], x[3]); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = r; }
 };
 
-// A thread's item is eight pairs of a head: the 8-element pieces at 8c and
-// rot/2 + 8c, or (INTER) the 16 elements at 16c; past rot, two pieces to copy.
-// Needs rot % 16 == 0.  grid: (total * HG) items of d / 16 threads; a thread
-// walks heads hg, hg + HG, ... (HPT of them), query heads first, then key heads.
+// A head has d / 2W couples of vectors, 8 / W of them a thread: couple p is the
+// vectors at W p and rot/2 + W p (W pairs), or (INTER) those at W p and d/2 + W p (W/2
+// pairs each); elements past rot are copied.  Needs rot % 16 == 0.  A thread walks
+// heads hg, hg + HG, ... (HPT of them) of its token, query heads first, then key heads.
 template <typename T, bool INTER, int HPT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Args a, uint32_t HG, int nc_shift) {
+  constexpr int W = Vec<T>::W, S = 8 / W;
   __shared__ uint64_t turns[INFLLM2_ROPE_MAX_PAIRS];
   const int c = threadIdx.x & ((1 << nc_shift) - 1);
   const uint32_t item = blockIdx.x * (kThreads >> nc_shift) + (threadIdx.x >> nc_shift);
@@ -113,71 +112,87 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const bool live = t < static_cast<uint32_t>(a.total);
   if (threadIdx.x < a.rot / 2) turns[threadIdx.x] = a.turns[threadIdx.x];
   const int half = a.rot >> 1;
-  const bool turn = 16 * c < a.rot;
-  const int e0 = (INTER || !turn) ? 16 * c : 8 * c;
-  const int e1 = (INTER || !turn) ? 16 * c + 8 : half + 8 * c;
+  int e0[S], e1[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int p = c + (s << nc_shift), past = p - half / W;
+    if (INTER) {
+      e0[s] = W * p;
+      e1[s] = (a.d >> 1) + W * p;
+    } else {
+      e0[s] = past < 0 ? W * p : a.rot + W * past;
+      e1[s] = past < 0 ? half + W * p : a.rot + ((a.d - a.rot) >> 1) + W * past;
+    }
+  }
 
-  Vec8<T> x0[HPT], x1[HPT];
-  int32_t p[4] = {0, 0, 0, 0};
+  Vec<T> x0[HPT][S], x1[HPT][S];
+  int32_t ps[4] = {0, 0, 0, 0};
   const int heads = a.h_q + a.h_kv;
   if (live) {
     for (int ax = 0; ax < 4; ++ax)
-      if (ax < a.n_axes) p[ax] = __ldg(a.pos + static_cast<int64_t>(ax) * a.total + t);
+      if (ax < a.n_axes) ps[ax] = __ldg(a.pos + static_cast<int64_t>(ax) * a.total + t);
 #pragma unroll
     for (int j = 0; j < HPT; ++j) {
       const int h = hg + j * HG;
       if (h < heads) {
         const T* row = h < a.h_q ? static_cast<const T*>(a.q) + (static_cast<int64_t>(t) * a.h_q + h) * a.d
                                  : static_cast<const T*>(a.k) + (static_cast<int64_t>(t) * a.h_kv + (h - a.h_q)) * a.d;
-        x0[j].load(row + e0);
-        x1[j].load(row + e1);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          x0[j][s].load(row + e0[s]);
+          x1[j][s].load(row + e1[s]);
+        }
       }
     }
   }
   __syncthreads();
   if (!live) return;
-  float sn[8], cs[8];
-  if (turn) {
+  float sn[S][W], cs[S][W];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int pair = 8 * c + i;
-      const int ps = pair >= a.bound[2] ? p[3] : pair >= a.bound[1] ? p[2] : pair >= a.bound[0] ? p[1] : p[0];
-      sincos_turns(angle(ps, turns[pair]), sn[i], cs[i]);
-      if (a.back) sn[i] = -sn[i];
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      // (past rot: no turn)
+      const int pair = !INTER ? e0[s] + i : i < W / 2 ? e0[s] / 2 + i : e1[s] / 2 + i - W / 2;
+      const int pos = pair >= a.bound[2] ? ps[3] : pair >= a.bound[1] ? ps[2] : pair >= a.bound[0] ? ps[1] : ps[0];
+      sn[s][i] = 0.f;
+      cs[s][i] = 1.f;
+      if (pair < half) sincos_turns(angle(pos, turns[pair]), sn[s][i], cs[s][i]);
+      if (a.back) sn[s][i] = -sn[s][i];
     }
-  }
 #pragma unroll
   for (int j = 0; j < HPT; ++j) {
     const int h = hg + j * HG;
     if (h < heads) {
-      if (turn) {
-        float u[8], v[8];
-        x0[j].get(u);
-        x1[j].get(v);
-        if (INTER) {
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float ua = u[i], ub = u[i + 1], va = v[i], vb = v[i + 1];
-            u[i] = ua * cs[i / 2] - ub * sn[i / 2];
-            u[i + 1] = ub * cs[i / 2] + ua * sn[i / 2];
-            v[i] = va * cs[4 + i / 2] - vb * sn[4 + i / 2];
-            v[i + 1] = vb * cs[4 + i / 2] + va * sn[4 + i / 2];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float ua = u[i], va = v[i];
-            u[i] = ua * cs[i] - va * sn[i];
-            v[i] = va * cs[i] + ua * sn[i];
-          }
-        }
-        x0[j].set(u);
-        x1[j].set(v);
-      }
       T* row = h < a.h_q ? static_cast<T*>(a.q_out) + (static_cast<int64_t>(t) * a.h_q + h) * a.d
                          : static_cast<T*>(a.k_out) + (static_cast<int64_t>(t) * a.h_kv + (h - a.h_q)) * a.d;
-      x0[j].store(row + e0);
-      x1[j].store(row + e1);
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        float u[W], v[W];
+        if (INTER) {
+          if (e0[s] < a.rot) {
+            x0[j][s].get(u);
+#pragma unroll
+            for (int i = 0; i < W; i += 2) turn_pair(u[i], u[i + 1], cs[s][i / 2], sn[s][i / 2]);
+            x0[j][s].set(u);
+          }
+          if (e1[s] < a.rot) {
+            x1[j][s].get(v);
+#pragma unroll
+            for (int i = 0; i < W; i += 2) turn_pair(v[i], v[i + 1], cs[s][(W + i) / 2], sn[s][(W + i) / 2]);
+            x1[j][s].set(v);
+          }
+        } else if (e0[s] < half) {
+          x0[j][s].get(u);
+          x1[j][s].get(v);
+#pragma unroll
+          for (int i = 0; i < W; ++i) turn_pair(u[i], v[i], cs[s][i], sn[s][i]);
+          x0[j][s].set(u);
+          x1[j][s].set(v);
+        }
+        x0[j][s].store(row + e0[s]);
+        x1[j][s].store(row + e1[s]);
+      }
     }
   }
 }
@@ -217,15 +232,16 @@ template <typename T, bool INTER>
 static cudaError_t launch_rope_typed(const rope::Args& a, cudaStream_t st) {
   const int nc = a.d / 16, nc_shift = a.d == 128 ? 3 : 2;
   const int64_t heads = static_cast<int64_t>(a.h_q) + a.h_kv;
-  // four heads a thread share the sines and cosines once the grid still fills
-  // the GPU (a wave of 2048 threads an SM); below that, a head a thread
-  const bool many = static_cast<int64_t>(a.total) * heads * nc / 4 >= static_cast<int64_t>(num_sms()) * 2048;
-  const int64_t HG = many ? (heads + 3) / 4 : heads;
+  // several heads a thread (128 bytes each way) share the sines and cosines once
+  // the grid still fills the GPU (a wave of 2048 threads an SM); below that, a head a thread
+  constexpr int kMany = sizeof(T) == 2 ? 4 : 2;
+  const bool many = static_cast<int64_t>(a.total) * heads * nc / kMany >= static_cast<int64_t>(num_sms()) * 2048;
+  const int64_t HG = many ? (heads + kMany - 1) / kMany : heads;
   const int64_t items = static_cast<int64_t>(a.total) * HG;
   const int per = rope::kThreads / nc;
   const unsigned grid = static_cast<unsigned>((items + per - 1) / per);
   if (many)
-    rope::rope_kernel<T, INTER, 4><<<grid, rope::kThreads, 0, st>>>(a, static_cast<uint32_t>(HG), nc_shift);
+    rope::rope_kernel<T, INTER, kMany><<<grid, rope::kThreads, 0, st>>>(a, static_cast<uint32_t>(HG), nc_shift);
   else
     rope::rope_kernel<T, INTER, 1><<<grid, rope::kThreads, 0, st>>>(a, static_cast<uint32_t>(HG), nc_shift);
   return cudaGetLastError();
