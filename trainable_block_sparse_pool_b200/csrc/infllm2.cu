@@ -475,8 +475,8 @@ static int check_paged_cache(const infllm2_paged_cache* c) {
     return INFLLM2_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128) return INFLLM2_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return INFLLM2_ERR_UNSUPPORTED;
-  // positions stay in 31 bits, units of 16 tokens past the end included
-  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - 1024) return INFLLM2_ERR_UNSUPPORTED;
+  // positions stay in 31 bits, a tile past the end included
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - 4096) return INFLLM2_ERR_UNSUPPORTED;
   return INFLLM2_OK;
 }
 

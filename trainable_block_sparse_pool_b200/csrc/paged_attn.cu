@@ -185,6 +185,7 @@ struct Walk {
   int b, g, n, t, te;   // sequence, kv head, its tiles, the next one, end of this piece
   int64_t left;         // cost of the range from the end of this piece on
   int tok_end;          // tokens of the piece end here
+  const int32_t* row;   // the sequence's pages
 };
 
 // the piece of pair (b, g) from cost position y on; false when the range covers none of its tiles
@@ -195,6 +196,7 @@ __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w, int y) {
   w.t = max(y - 1, 0);
   w.te = y + take - 1;
   w.tok_end = min(__ldg(a.len + w.b), w.te * kTile);
+  w.row = a.table + static_cast<int64_t>(w.b) * a.max_pages;
   return w.t < w.te;
 }
 
@@ -215,45 +217,63 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
   return ++w.t < w.te || walk_pair<kTile>(a, w);
 }
 
-// the page of every 16-token group of the walk's tile (-1: no token of the piece in it)
+// The pages of the walk's tile: one where pages hold whole tiles, else one for every 16-token group
+// (-1: no token of the piece in it).  Nothing here waits for them.
 template <int kTile>
 __device__ __forceinline__ void fetch_pages(const Args& a, const Walk& w, int (&page)[kTile / kUnit]) {
-  const int32_t* row = a.table + static_cast<int64_t>(w.b) * a.max_pages;
+  const int tok0 = w.t * kTile;
+  page[0] = __ldg(w.row + (tok0 >> a.page_shift));
+  if ((kTile >> a.page_shift) > 1) {
 #pragma unroll
-  for (int i = 0; i < kTile / kUnit; ++i)
-    page[i] = w.t * kTile + i * kUnit < w.tok_end ? __ldg(row + ((w.t * kTile + i * kUnit) >> a.page_shift)) : -1;
+    for (int i = 1; i < kTile / kUnit; ++i) {
+      page[i] = -1;
+      if (tok0 + i * kUnit < w.tok_end) page[i] = __ldg(w.row + ((tok0 + i * kUnit) >> a.page_shift));
+    }
+  }
 }
 
+// Instruction i copies the S tokens of lane group i, 512 contiguous bytes, for K
+// and for V.  piece_at of the eight differs by i * 512 and an XOR of the lane's
+// part with 16 f(i), which takes few values.
 template <int D, bool F8>
 __device__ __forceinline__ void issue_tile(const Args& a, const Walk& w, const int (&page)[Cfg<D, F8>::kTile / kUnit],
                                            uint32_t stage, int lane) {
   using C = Cfg<D, F8>;
   constexpr int NG = C::kTile / kUnit;   // 16-token groups
-  constexpr int IPG = 8 / NG;            // instructions a group: 512 contiguous bytes each
+  constexpr int IPG = 8 / NG;            // instructions a group
   const int tok0 = w.t * C::kTile;
   const int nv = min(C::kTile, w.tok_end - tok0);
-  const int mask = (1 << a.page_shift) - 1;
+  const int slot0 = tok0 & ((1 << a.page_shift) - 1);
+  const bool one = (C::kTile >> a.page_shift) <= 1;
+  int pg[NG];
+#pragma unroll
+  for (int i = 0; i < NG; ++i) pg[i] = i == 0 || one ? page[0] : page[i];
   const int r0 = lane / C::CH, c = lane % C::CH;   // instruction i: tokens S i + r0
   int64_t at[NG];                        // first row of the group
   bool ok = nv == C::kTile;
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
-    at[i] = ((static_cast<int64_t>(page[i]) * a.h_kv + w.g) << a.page_shift) + ((tok0 + i * kUnit) & mask);
-    ok = ok && page[i] >= 0 && page[i] < a.n_pages;
+    at[i] = ((static_cast<int64_t>(pg[i]) * a.h_kv + w.g) << a.page_shift) +
+            ((slot0 + i * kUnit) & ((1 << a.page_shift) - 1));
+    ok = ok && static_cast<unsigned>(pg[i]) < static_cast<unsigned>(a.n_pages);
   }
   if (ok) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t off = at[i / IPG] * C::kRow + (i % IPG) * 512 + lane * 16;
-      const uint32_t dst = stage + piece_at<C::CH, C::S, F8>(i, r0, c);
-      cp_async16_full(dst, a.k_pages + off);
-      cp_async16_full(dst + kHalf, a.v_pages + off);
+    for (int g = 0; g < NG; ++g) {
+      const uint8_t* k = a.k_pages + (at[g] * C::kRow + lane * 16);
+      const uint8_t* v = a.v_pages + (at[g] * C::kRow + lane * 16);
+#pragma unroll
+      for (int j = 0; j < IPG; ++j) {
+        const int i = g * IPG + j;
+        const uint32_t dst = stage + piece_at<C::CH, C::S, F8>(i, r0, c);
+        cp_async16_full(dst, k + j * 512);
+        cp_async16_full(dst + kHalf, v + j * 512);
+      }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int pg = page[i / IPG];
-      const bool in = C::S * i + r0 < nv, good = pg >= 0 && pg < a.n_pages;
+      const bool in = C::S * i + r0 < nv, good = static_cast<unsigned>(pg[i / IPG]) < static_cast<unsigned>(a.n_pages);
       if (in && !good) record_status(INFLLM2_ERR_DEVICE_BOUNDS);
       const int64_t off = in && good ? at[i / IPG] * C::kRow + (i % IPG) * 512 + lane * 16 : 0;
       const uint32_t dst = stage + piece_at<C::CH, C::S, F8>(i, r0, c);
@@ -267,11 +287,12 @@ __device__ __forceinline__ void issue_tile(const Args& a, const Walk& w, const i
     if (lane < 2 * P) {
       const int t = 4 * (lane % P);
       int64_t row = at[0];
-      int pg = page[0];
+      int of = pg[0];
 #pragma unroll
       for (int i = 1; i < NG; ++i)
-        if (t / kUnit == i) { row = at[i]; pg = page[i]; }
-      const int bytes = pg >= 0 && pg < a.n_pages ? max(0, min(16, 4 * (nv - t))) : 0;
+        if (t / kUnit == i) { row = at[i]; of = pg[i]; }
+      const bool good = static_cast<unsigned>(of) < static_cast<unsigned>(a.n_pages);
+      const int bytes = good ? max(0, min(16, 4 * (nv - t))) : 0;
       const float* src = lane < P ? a.k_scale : a.v_scale;
       cp_async16_part(stage + 2 * kHalf + lane * 16, bytes > 0 ? src + row + (t & (kUnit - 1)) : src, bytes);
     }
