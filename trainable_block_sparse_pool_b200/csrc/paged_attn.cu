@@ -574,8 +574,13 @@ __device__ __forceinline__ void tile_pin(State<D, F8, NH>& st) {
   }
 }
 
-// The G heads' normalised rows and log-sum-exps: to `mine` (G rows, then G log-sum-exps); with mine null to the
-// pair's rows of the output (`out`) or to partial `slot`.
+// Floats from one row of a partial in shared memory to the next: the lanes of a store (rows 2 tig, columns by
+// gid) then meet all banks.
+template <int D>
+constexpr int kPartLd = D + 4;
+
+// The G heads' normalised rows and log-sum-exps: to `mine` (G rows of kPartLd floats, then G log-sum-exps); with
+// mine null to the pair's rows of the output (`out`) or to partial `slot`.
 template <int D, bool F8, int NH>
 __device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st, float* mine, bool out, int pair,
                                             int64_t slot, int lane) {
@@ -595,8 +600,8 @@ __device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st,
       if (F8) inv *= __uint_as_float(static_cast<uint32_t>(st.e_r - 11) << 23);
       const float lse = l == 0.f ? -INFINITY : st.m[nh][e] + log2f(l);
       const int64_t row = (out ? pair : slot) * a.G + h;
-      float* po = mine ? mine + h * D : (!out ? a.part_o : a.out_f32 ? static_cast<float*>(a.out) : nullptr) + row * D;
-      float* pl = mine ? mine + a.G * D + h : (out ? a.lse : a.part_lse) + row;
+      float* po = mine ? mine + h * kPartLd<D> : (!out ? a.part_o : a.out_f32 ? static_cast<float*>(a.out) : nullptr) + row * D;
+      float* pl = mine ? mine + a.G * kPartLd<D> + h : (out ? a.lse : a.part_lse) + row;
       const bool b16 = !mine && out && !a.out_f32;
       if (gid == 0 && (mine || !out || a.lse)) *pl = lse;
       __nv_bfloat16* pb = static_cast<__nv_bfloat16*>(a.out) + row * D;
@@ -767,14 +772,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     const int len = w1 - w0 + 1;
     const int64_t row0 = (out ? head.x : 2 * static_cast<int64_t>(blockIdx.x * kWarps + w0) + (head.y ? 1 : 0)) * a.G;
     for (int i = threadIdx.x; i < a.G * (D / 4); i += 32 * kWarps) {
-      const int h = i / (D / 4);
-      float4 o = reinterpret_cast<const float4*>(part)[i];
-      float lse = part[a.G * D + h];
+      const int h = i / (D / 4), at4 = h * (kPartLd<D> / 4) + i % (D / 4);
+      float4 o = reinterpret_cast<const float4*>(part)[at4];
+      float lse = part[a.G * kPartLd<D> + h];
       if (len > 1) {
         float x[kWarps], m = lse;
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
-          x[w] = part[min(w, len - 1) * kWarpFloats + a.G * D + h];
+          x[w] = part[min(w, len - 1) * kWarpFloats + a.G * kPartLd<D> + h];
           m = fmaxf(m, x[w]);
         }
         const float ref = m == -INFINITY ? 0.f : m;
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
         for (int w = 1; w < kWarps; ++w)
           if (w < len) {
             const float f = ex2(x[w] - ref);
-            const float4 v = reinterpret_cast<const float4*>(part + w * kWarpFloats)[i];
+            const float4 v = reinterpret_cast<const float4*>(part + w * kWarpFloats)[at4];
             l += f;
             o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
           }
