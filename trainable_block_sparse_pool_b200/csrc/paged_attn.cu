@@ -574,37 +574,69 @@ __device__ __forceinline__ void tile_pin(State<D, F8, NH>& st) {
   }
 }
 
-// Floats from one row of a partial in shared memory to the next: the lanes of a store (rows 2 tig, columns by
+// Floats from one row of a partial in shared memory to the next: the lanes of a store (rows by tig, columns by
 // gid) then meet all banks.
 template <int D>
 constexpr int kPartLd = D + 4;
 
-// The G heads' normalised rows and log-sum-exps: to `mine` (G rows of kPartLd floats, then G log-sum-exps); with
-// mine null to the pair's rows of the output (`out`) or to partial `slot`.
+// A row's sum over the lanes that share it: the factor that normalises O^T, and the log-sum-exp.
+// l = 0: every score was -inf; the row is empty.
 template <int D, bool F8, int NH>
-__device__ __forceinline__ void write_piece(const Args& a, State<D, F8, NH>& st, float* mine, bool out, int pair,
+__device__ __forceinline__ void row_stats(const State<D, F8, NH>& st, int nh, int e, float& inv, float& lse) {
+  float l = st.l[nh][e];
+  l += __shfl_xor_sync(0xffffffffu, l, 4);
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
+  inv = l == 0.f ? 0.f : 1.f / l;
+  if (F8) inv *= __uint_as_float(static_cast<uint32_t>(st.e_r - 11) << 23);
+  lse = l == 0.f ? -INFINITY : st.m[nh][e] + log2f(l);
+}
+
+// The normalised rows of all 8 NH heads (of which G are real) to shared memory, then their log-sum-exps.  Kept apart
+// from write_piece: every warp runs this once, from a cold instruction cache, so it is short.
+template <int D, bool F8, int NH>
+__device__ __forceinline__ void keep_piece(const State<D, F8, NH>& st, float* mine, int lane) {
+  const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+  for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float inv, lse;
+      row_stats(st, nh, e, inv, lse);
+      float* row = mine + (8 * nh + 2 * tig + e) * kPartLd<D>;
+      if (gid == 0) mine[8 * NH * kPartLd<D> + 8 * nh + 2 * tig + e] = lse;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        // F8: columns D/8 gid + 2 i + {0, 1}; else 16 i + gid + {0, 8}
+        const float v0 = st.o[nh][i][e] * inv, v1 = st.o[nh][i][2 + e] * inv;
+        if (F8) {
+          *reinterpret_cast<float2*>(row + D / 8 * gid + 2 * i) = make_float2(v0, v1);
+        } else {
+          row[16 * i + gid] = v0;
+          row[16 * i + 8 + gid] = v1;
+        }
+      }
+    }
+}
+
+// The G heads' normalised rows and log-sum-exps to the pair's rows of the output (`out`) or to partial `slot`.
+template <int D, bool F8, int NH>
+__device__ __forceinline__ void write_piece(const Args& a, const State<D, F8, NH>& st, bool out, int pair,
                                             int64_t slot, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float l = st.l[nh][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      float inv, lse;
+      row_stats(st, nh, e, inv, lse);
       const int h = 2 * tig + e + 8 * nh;
       if (h >= a.G) continue;
-      // l = 0: every score was -inf; the row is empty
-      float inv = l == 0.f ? 0.f : 1.f / l;
-      if (F8) inv *= __uint_as_float(static_cast<uint32_t>(st.e_r - 11) << 23);
-      const float lse = l == 0.f ? -INFINITY : st.m[nh][e] + log2f(l);
       const int64_t row = (out ? pair : slot) * a.G + h;
-      float* po = mine ? mine + h * kPartLd<D> : (!out ? a.part_o : a.out_f32 ? static_cast<float*>(a.out) : nullptr) + row * D;
-      float* pl = mine ? mine + a.G * kPartLd<D> + h : (out ? a.lse : a.part_lse) + row;
-      const bool b16 = !mine && out && !a.out_f32;
-      if (gid == 0 && (mine || !out || a.lse)) *pl = lse;
+      const bool b16 = out && !a.out_f32;
+      float* po = (!out ? a.part_o : static_cast<float*>(a.out)) + row * D;
       __nv_bfloat16* pb = static_cast<__nv_bfloat16*>(a.out) + row * D;
+      if (gid == 0 && (!out || a.lse)) (out ? a.lse : a.part_lse)[row] = lse;
       if (F8) {
         // columns D/8 gid .. D/8 (gid + 1)
 #pragma unroll
@@ -744,8 +776,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
       rest = cons.n - cons.te;
       // the range's last piece waits in this warp's share of the ring; an earlier one ends its pair
       const bool keep = cons.left <= 1;   // (what is left is no other pair's tile)
-      write_piece<D, F8, NH>(a, st, keep ? reinterpret_cast<float*>(smem + warp * kStages * C::kStage) : nullptr,
-                             from0, pair, 2 * static_cast<int64_t>(wk), lane);
+      if (keep)
+        keep_piece<D, F8, NH>(st, reinterpret_cast<float*>(smem + warp * kStages * C::kStage), lane);
+      else
+        write_piece<D, F8, NH>(a, st, from0, pair, 2 * static_cast<int64_t>(wk), lane);
       if (!keep && from0 && a.by_pair && lane == 0) a.desc[pair] = make_int4(0, 0, -1, 0);
     }
     run = walk_next<C::kTile>(a, cons);
@@ -774,12 +808,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     for (int i = threadIdx.x; i < a.G * (D / 4); i += 32 * kWarps) {
       const int h = i / (D / 4), at4 = h * (kPartLd<D> / 4) + i % (D / 4);
       float4 o = reinterpret_cast<const float4*>(part)[at4];
-      float lse = part[a.G * kPartLd<D> + h];
+      float lse = part[8 * NH * kPartLd<D> + h];
       if (len > 1) {
         float x[kWarps], m = lse;
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
-          x[w] = part[min(w, len - 1) * kWarpFloats + a.G * kPartLd<D> + h];
+          x[w] = part[min(w, len - 1) * kWarpFloats + 8 * NH * kPartLd<D> + h];
           m = fmaxf(m, x[w]);
         }
         const float ref = m == -INFINITY ? 0.f : m;
