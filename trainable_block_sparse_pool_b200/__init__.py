@@ -380,6 +380,11 @@ def infllm2_decode_step(st: DecodeState, q: torch.Tensor, k_new: torch.Tensor, v
 
 
 # ------------------------------------------------------------------ rotary positions, paged cache
+# (These calls check every tensor they are given.  The checks are plain attribute reads: on a short call they, the
+# argument conversion and the launch take about 2 us each, more than the kernel.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # noqa: SLF001  (current_stream(), unwrapped)
+
+
 def _expect(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
     """The data pointer of a contiguous tensor of this dtype and shape on CUDA device `device` (-1: the CPU); raises
     otherwise."""
@@ -389,28 +394,11 @@ def _expect(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
     return t.data_ptr()
 
 
-def _cuda(t: torch.Tensor) -> int:
-    """The tensor's CUDA device; the library has no CPU path, so a tensor elsewhere is refused."""
-    i = t.get_device()
-    if i < 0:
-        raise InfLLM2Error(f"expected CUDA tensors, got one on {t.device}")
-    return i
-
-
-def _launch(name: str, device: int, stream, *args) -> None:
-    """One library call with `device` current (a launch goes to the current device), on `stream` or its current one."""
-    f = getattr(lib(), name)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)  # noqa: SLF001  (current_stream() without its wrapper)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    if torch.cuda.current_device() == device:
-        rc = f(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, stream)
-    if rc != 0:
-        _check(name, rc)
+def _elsewhere(device: int) -> bool:
+    """Whether `device` (a tensor's) is not the current one, to which a launch goes; refuses the CPU."""
+    if device < 0:
+        raise InfLLM2Error("expected CUDA tensors: the library has no CPU path")
+    return device != torch.cuda.current_device()
 
 
 def make_rope(rot: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None, interleaved: bool = False,
@@ -432,16 +420,22 @@ def make_rope(rot: int, base: float = 10000.0, sections: Optional[Sequence[int]]
 
 
 def _rope(name: str, q, k, pos, rope, q_out, k_out, stream) -> None:
-    dev, dt, qs, ks = _cuda(q), q.dtype, q.shape, k.shape
+    dev, dt, qs, ks = q.get_device(), q.dtype, q.shape, k.shape
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _rope(name, q, k, pos, rope, q_out, k_out, stream)
     if len(qs) != 3 or len(ks) != 3 or not (dt is torch.bfloat16 or dt is torch.float32):
         raise InfLLM2Error(f"{name}: q and k are [total, heads, d] tensors of bf16 or fp32")
     total, h_q, d = qs
     h_kv, axes = ks[1], rope.n_axes
-    _launch(name, dev, stream, _expect("q", q, dt, qs, dev), _expect("k", k, dt, (total, h_kv, d), dev),
-            OUT_BF16 if dt is torch.bfloat16 else OUT_F32,
-            _expect("pos", pos, torch.int32, (total,) if axes == 1 and pos.dim() == 1 else (axes, total), dev),
-            total, h_q, h_kv, d, ctypes.byref(rope), _expect("q_out", q_out, dt, qs, dev),
-            _expect("k_out", k_out, dt, ks, dev))
+    rc = getattr(lib(), name)(
+        _expect("q", q, dt, qs, dev), _expect("k", k, dt, (total, h_kv, d), dev),
+        OUT_BF16 if dt is torch.bfloat16 else OUT_F32,
+        _expect("pos", pos, torch.int32, (total,) if axes == 1 and pos.dim() == 1 else (axes, total), dev),
+        total, h_q, h_kv, d, ctypes.byref(rope), _expect("q_out", q_out, dt, qs, dev),
+        _expect("k_out", k_out, dt, ks, dev), _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(name, rc)
 
 
 def infllm2_rope(q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, rope: RopeSpec, q_out: torch.Tensor,
@@ -487,30 +481,43 @@ def infllm2_paged_write(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, sta
                         cu_seqlens: Optional[torch.Tensor] = None, stream=None) -> None:
     """Writes packed rows K, V [total, h_kv, d] (bf16) into the pages: row i of sequence b goes to position
     start[b] + i.  cu_seqlens int32 [batch + 1]; None: one row a sequence."""
-    _cuda(K)
     dev, batch, total = cache._device, cache.batch, K.shape[0]  # noqa: SLF001
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return infllm2_paged_write(cache, K, V, start, cu_seqlens, stream)
     shape = (total, cache.h_kv, cache.d)
-    _launch("infllm2_paged_write", dev, stream, ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev),
-            _expect("V", V, torch.bfloat16, shape, dev), _expect("start", start, torch.int32, (batch,), dev),
-            None if cu_seqlens is None else _expect("cu_seqlens", cu_seqlens, torch.int32, (batch + 1,), dev), total)
+    rc = lib().infllm2_paged_write(
+        ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev), _expect("V", V, torch.bfloat16, shape, dev),
+        _expect("start", start, torch.int32, (batch,), dev),
+        None if cu_seqlens is None else _expect("cu_seqlens", cu_seqlens, torch.int32, (batch + 1,), dev), total,
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check("infllm2_paged_write", rc)
 
 
 def infllm2_paged_read(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, cu_seqlens: torch.Tensor,
                        stream=None) -> None:
     """Reads positions 0 .. len-1 of every sequence into the packed rows of K, V [total, h_kv, d] (bf16)."""
-    _cuda(K)
     dev, total = cache._device, K.shape[0]  # noqa: SLF001
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return infllm2_paged_read(cache, K, V, cu_seqlens, stream)
     shape = (total, cache.h_kv, cache.d)
-    _launch("infllm2_paged_read", dev, stream, ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev),
-            _expect("V", V, torch.bfloat16, shape, dev),
-            _expect("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), dev), total)
+    rc = lib().infllm2_paged_read(
+        ctypes.byref(cache), _expect("K", K, torch.bfloat16, shape, dev), _expect("V", V, torch.bfloat16, shape, dev),
+        _expect("cu_seqlens", cu_seqlens, torch.int32, (cache.batch + 1,), dev), total,
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check("infllm2_paged_read", rc)
 
 
 def infllm2_paged_workspace_bytes(cache: PagedCache, h_q: int) -> int:
-    if cache._device < 0:  # noqa: SLF001
-        raise InfLLM2Error("the cache's tensors are not on a CUDA device")
-    with torch.cuda.device(cache._device):  # noqa: SLF001
-        return int(lib().infllm2_paged_workspace_bytes(ctypes.byref(cache), h_q))
+    """Bytes of the workspace of infllm2_paged_decode_attn on the cache's device; 0 for an unsupported shape."""
+    dev = cache._device  # noqa: SLF001
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return infllm2_paged_workspace_bytes(cache, h_q)
+    return int(lib().infllm2_paged_workspace_bytes(ctypes.byref(cache), h_q))
 
 
 _DEFAULTS: Optional[Params] = None
@@ -522,19 +529,24 @@ def infllm2_paged_decode_attn(cache: PagedCache, q: torch.Tensor, seq_len: torch
     """Attention of one token a sequence, q [batch, h_q, d] (bf16), over the first seq_len[b] positions of its pages
     (its own row among them) into out [batch, h_q, d] (bf16 or fp32) and, if given, lse fp32 [batch, h_q]."""
     global _DEFAULTS
+    dev, batch, od, qs = cache._device, cache.batch, out.dtype, q.shape  # noqa: SLF001
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return infllm2_paged_decode_attn(cache, q, seq_len, out, workspace, lse, params, stream)
+    if len(qs) != 3 or not (od is torch.bfloat16 or od is torch.float32):
+        raise InfLLM2Error("q is [batch, h_q, d], out bf16 or fp32")
     if params is None:
         if _DEFAULTS is None:
             _DEFAULTS = default_params()
         params = _DEFAULTS
-    _cuda(q)
-    dev, batch, od = cache._device, cache.batch, out.dtype  # noqa: SLF001
-    if q.dim() != 3 or not (od is torch.bfloat16 or od is torch.float32):
-        raise InfLLM2Error("q is [batch, h_q, d], out bf16 or fp32")
-    h_q = q.shape[1]
+    h_q = qs[1]
     shape = (batch, h_q, cache.d)
-    _launch("infllm2_paged_decode_attn", dev, stream, ctypes.byref(cache), _expect("q", q, torch.bfloat16, shape, dev),
-            h_q, _expect("seq_len", seq_len, torch.int32, (batch,), dev), _expect("out", out, od, shape, dev),
-            OUT_BF16 if od is torch.bfloat16 else OUT_F32,
-            None if lse is None else _expect("lse", lse, torch.float32, (batch, h_q), dev),
-            _expect("workspace", workspace, workspace.dtype, workspace.shape, dev), workspace.nbytes,
-            ctypes.byref(params))
+    rc = lib().infllm2_paged_decode_attn(
+        ctypes.byref(cache), _expect("q", q, torch.bfloat16, shape, dev), h_q,
+        _expect("seq_len", seq_len, torch.int32, (batch,), dev), _expect("out", out, od, shape, dev),
+        OUT_BF16 if od is torch.bfloat16 else OUT_F32,
+        None if lse is None else _expect("lse", lse, torch.float32, (batch, h_q), dev),
+        _expect("workspace", workspace, workspace.dtype, workspace.shape, dev), workspace.nbytes, ctypes.byref(params),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check("infllm2_paged_decode_attn", rc)
