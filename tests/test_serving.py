@@ -480,6 +480,67 @@ def test_decode_attention_with_uneven_rows(d, e4m3):
 
 
 @gpu
+def test_many_short_sequences_and_shared_pages():
+    # more sequences than a CTA has threads; pages that several sequences share, at several lengths
+    page, h_q, h_kv, d = 16, 4, 2, 64
+    pages, scales, _ = _pages([4096], h_kv, d, page, False, 17)
+    g = torch.Generator().manual_seed(6)
+    lens = torch.randint(0, 49, (3000,), generator=g).tolist()
+    table = torch.randint(0, 256, (3000, 3), generator=g, dtype=torch.int32).cuda()
+    pages = [p.nan_to_num(0.25) for p in pages]
+    cache = T.make_paged_cache(*pages, table)
+    q = torch.randn(3000, h_q, d, device="cuda").bfloat16()
+    out, lse = torch.empty(3000, h_q, d, device="cuda"), torch.empty(3000, h_q, device="cuda")
+    ws = torch.empty(T.infllm2_paged_workspace_bytes(cache, h_q), dtype=torch.uint8, device="cuda")
+    T.infllm2_paged_decode_attn(cache, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), out, ws, lse)
+    # all sequences at once: [batch, h_kv, 48, d]
+    k, v = (p[table.long()].double().transpose(1, 2).reshape(3000, h_kv, 48, d).repeat_interleave(2, 1) for p in pages)
+    n = torch.tensor(lens, device="cuda")
+    z = (q.double()[:, :, None] @ k.transpose(2, 3))[:, :, 0] / 8
+    z = z.masked_fill(torch.arange(48, device="cuda") >= n[:, None, None], -math.inf)
+    m = torch.logsumexp(z, -1)
+    p = torch.exp(z - m.clamp(min=-1e300)[..., None])
+    mag = (q.double().abs()[:, :, None] @ k.abs().transpose(2, 3))[:, :, 0].amax(-1) / 8 / math.log(2)
+    _check(out, lse, ((p[:, :, None] @ v)[:, :, 0], m / math.log(2), (p[:, :, None] @ v.abs())[:, :, 0], mag), d, 48, False)
+
+
+@gpu
+def test_calls_on_a_given_stream_and_with_no_tokens():
+    pages, scales, table = _pages([100, 30], 2, 64, 16, True, 2)
+    cache = T.make_paged_cache(*pages, table, *scales)
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    n = torch.tensor([100, 30], dtype=torch.int32, device="cuda")
+    outs = [torch.empty(2, 4, 64, device="cuda") for _ in range(2)]
+    wss = [torch.empty(T.infllm2_paged_workspace_bytes(cache, 4), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    K = torch.randn(130, 2, 64, device="cuda").bfloat16()
+    got, cu = torch.empty_like(K), torch.tensor([0, 100, 130], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    T.infllm2_paged_write(cache, K, K, torch.zeros_like(n), cu, stream=side)
+    T.infllm2_paged_read(cache, got, torch.empty_like(K), cu, stream=side)
+    T.infllm2_paged_decode_attn(cache, q, n, outs[0], wss[0], stream=side)
+    side.synchronize()
+    T.infllm2_paged_decode_attn(cache, q, n, outs[1], wss[1], stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1])
+    assert ((got.double() - K.double()).abs() <= K.double().abs() * 2.0 ** -3 + 2.0 ** -8).all()
+    # nothing to write, read or turn
+    none, zero = K[:0], torch.zeros(3, dtype=torch.int32, device="cuda")
+    T.infllm2_paged_write(cache, none, none, torch.zeros_like(n), zero)
+    T.infllm2_paged_read(cache, none, none, zero)
+    T.infllm2_rope(none, none, torch.zeros(1, 0, dtype=torch.int32, device="cuda"), T.make_rope(64), none, none)
+    # a tensor that starts off a 16-byte boundary, on another device, of another type
+    odd = torch.empty(2 * 4 * 64 + 1, device="cuda", dtype=torch.bfloat16)[1:].view(2, 4, 64)
+    for bad in (odd, q.cpu(), q.float(), q[:, :3]):
+        with pytest.raises(T.InfLLM2Error):
+            T.infllm2_paged_decode_attn(cache, bad, n, outs[0], wss[0])
+    with pytest.raises(T.InfLLM2Error):
+        T.infllm2_paged_decode_attn(cache, q, n, outs[0], wss[0][:-16])
+    torch.cuda.synchronize()
+    assert T.infllm2_get_device_status() == 0
+
+
+@gpu
 def test_infinite_scores_and_nan_rows():
     pages, scales, table = _pages([40, 40, 33], 1, 64, 16, False, 4)
     k, v = pages

@@ -427,8 +427,9 @@ int infllm2_rope_init(infllm2_rope_spec* r, int32_t rot, int32_t n_axes, const i
 static int rope_common(const void* q, const void* k, int32_t dtype, const int32_t* pos, int64_t total, int32_t h_q,
                        int32_t h_kv, int32_t d, const infllm2_rope_spec* r, void* q_out, void* k_out, int back,
                        void* stream) {
-  if (!q || !k || !pos || !r || !q_out || !k_out || !aligned16(q) || !aligned16(k) || !aligned16(q_out) ||
-      !aligned16(k_out) || (reinterpret_cast<uintptr_t>(pos) & 3u))
+  // (with no tokens there is no memory to point at)
+  if (!r || (total != 0 && (!q || !k || !pos || !q_out || !k_out)) || !aligned16(q) || !aligned16(k) ||
+      !aligned16(q_out) || !aligned16(k_out) || (reinterpret_cast<uintptr_t>(pos) & 3u))
     return INFLLM2_ERR_INVALID_ARG;
   if (dtype != INFLLM2_OUT_BF16 && dtype != INFLLM2_OUT_F32) return INFLLM2_ERR_INVALID_ARG;
   if (total < 0 || h_q <= 0 || h_kv <= 0) return INFLLM2_ERR_INVALID_ARG;
@@ -486,13 +487,13 @@ static int page_shift(const infllm2_paged_cache* c) {
   return s;
 }
 
-static int paged_rows(const infllm2_paged_cache* c, const void* K, const void* V, void* Ko, void* Vo,
-                      const int32_t* start, const int32_t* cu_seqlens, int64_t total, void* stream) {
+// Writes K and V, or (write false) reads into them.
+static int paged_rows(const infllm2_paged_cache* c, bool write, const void* K, const void* V, const int32_t* start,
+                      const int32_t* cu_seqlens, int64_t total, void* stream) {
   int r;
   if ((r = check_paged_cache(c))) return r;
-  const void* k = K ? K : Ko;
-  const void* v = V ? V : Vo;
-  if (!k || !v || !aligned16(k) || !aligned16(v) || total < 0) return INFLLM2_ERR_INVALID_ARG;
+  // (with no rows there is no memory to point at)
+  if ((total != 0 && (!K || !V)) || !aligned16(K) || !aligned16(V) || total < 0) return INFLLM2_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
     return INFLLM2_ERR_INVALID_ARG;
   if (!cu_seqlens && total != c->batch) return INFLLM2_ERR_INVALID_ARG;
@@ -502,21 +503,21 @@ static int paged_rows(const infllm2_paged_cache* c, const void* K, const void* V
   a.k_scale = c->k_scale; a.v_scale = c->v_scale; a.table = c->block_table; a.cu = cu_seqlens; a.start = start;
   a.n_pages = c->n_pages; a.page_shift = page_shift(c); a.batch = c->batch; a.max_pages = c->max_pages;
   a.h_kv = c->h_kv; a.total = static_cast<int32_t>(total);
-  cudaError_t e = launch_paged_rows(a, c->d, c->dtype == INFLLM2_KV_E4M3, K, V, Ko, Vo,
+  cudaError_t e = launch_paged_rows(a, write, c->d, c->dtype == INFLLM2_KV_E4M3, K, V,
                                     static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? INFLLM2_OK : cuda_fail(e);
 }
 
 int infllm2_paged_write(const infllm2_paged_cache* c, const void* K, const void* V, const int32_t* start,
                         const int32_t* cu_seqlens, int64_t total, void* stream) {
-  if (!K || !V || !start) return INFLLM2_ERR_INVALID_ARG;
-  return paged_rows(c, K, V, nullptr, nullptr, start, cu_seqlens, total, stream);
+  if (!start) return INFLLM2_ERR_INVALID_ARG;
+  return paged_rows(c, true, K, V, start, cu_seqlens, total, stream);
 }
 
 int infllm2_paged_read(const infllm2_paged_cache* c, void* K, void* V, const int32_t* cu_seqlens, int64_t total,
                        void* stream) {
-  if (!K || !V || !cu_seqlens) return INFLLM2_ERR_INVALID_ARG;
-  return paged_rows(c, nullptr, nullptr, K, V, nullptr, cu_seqlens, total, stream);
+  if (!cu_seqlens) return INFLLM2_ERR_INVALID_ARG;
+  return paged_rows(c, false, K, V, nullptr, cu_seqlens, total, stream);
 }
 
 static int check_paged_heads(const infllm2_paged_cache* c, int32_t h_q) {

@@ -41,14 +41,8 @@ namespace pattn {
 using dec::cp_async_commit;
 using dec::cp_async_wait_n;
 
-#ifndef INFLLM2_PATTN_WARPS
-#define INFLLM2_PATTN_WARPS 8
-#endif
-#ifndef INFLLM2_PATTN_STAGES
-#define INFLLM2_PATTN_STAGES 3
-#endif
-constexpr int kWarps = INFLLM2_PATTN_WARPS;
-constexpr int kStages = INFLLM2_PATTN_STAGES;
+constexpr int kWarps = 8;
+constexpr int kStages = 3;
 constexpr int kUnit = 16;           // tokens; every page size is a multiple of it
 constexpr float kMargin = 4.f;      // the reference maximum is raised only past this many log2 units
 constexpr int kHalf = 4096;         // bytes of K, and of V, in a stage
@@ -200,13 +194,17 @@ __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w, int y) {
   return w.t < w.te;
 }
 
-// the first piece at or after pair (b, g); false when the range is done
+// the first piece after pair (b, g); false when the range is done (or, with lengths that change under the call, when
+// there is no further sequence)
 template <int kTile>
 __device__ __forceinline__ bool walk_pair(const Args& a, Walk& w) {
   if (w.left <= 0) return false;
   if (++w.g == a.h_kv) {
     w.g = 0;
-    do { ++w.b; w.n = seq_tiles<kTile>(a, w.b); } while (w.n == 0);
+    do {
+      if (++w.b >= a.batch) return false;
+      w.n = seq_tiles<kTile>(a, w.b);
+    } while (w.n == 0);
   }
   return walk_piece<kTile>(a, w, 0);   // an empty piece (the pair's start alone) ends its range
 }
@@ -725,17 +723,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     lo *= kWarps;
     lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < kWarps && chunk[lo + lane] <= x0));
     int64_t r = x0 - chunk[lo];
-    int64_t cost;
+    int64_t cost = 1;
     prod.b = lo * per;
-    for (;; ++prod.b) {
+    for (; prod.b < a.batch; ++prod.b) {
       prod.n = seq_tiles<C::kTile>(a, prod.b);
       cost = pair_cost(prod.n);
       if (r < cost * a.h_kv) break;
       r -= cost * a.h_kv;
     }
-    prod.g = static_cast<int>(div_pos(r, cost));
+    more = prod.b < a.batch;   // (lengths that change under the call)
+    prod.g = more ? static_cast<int>(div_pos(r, cost)) : 0;
     prod.left = x1 - x0;
-    more = walk_piece<C::kTile>(a, prod, static_cast<int>(r - prod.g * cost)) || walk_pair<C::kTile>(a, prod);
+    more = more && (walk_piece<C::kTile>(a, prod, static_cast<int>(r - prod.g * cost)) || walk_pair<C::kTile>(a, prod));
   }
   Walk cons = prod;
   const uint32_t ring = smem_u32(smem) + warp * kStages * C::kStage;
