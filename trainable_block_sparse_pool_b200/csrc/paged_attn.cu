@@ -32,6 +32,13 @@
 // probability: w_u = p_u * scale_u / R * 2^11 in f16, with R a power of two no
 // less than any scale seen and p_u <= 2^kMargin, so w keeps 11 bits where
 // p_u scale_u >= 2^-25 R.
+//
+// Measured (one B200, sustained): 16 x 131072 8-bit, 1.11 GB, 186-205 us (5.4-6.0
+// TB/s; 32 heads), 175-181 us with 8 heads a group; 16 x 65536 bf16, 1.07 GB, 172-177 us; 64 bf16
+// sequences up to 8192, 0.27 GB, 57 us; one sequence of 1000 9.5 us.  A tile of the first costs its warp
+// 1800 cycles of products and softmax and 750 of copies and bookkeeping, with two warps
+// a scheduler.  That fits within the bandwidth at full clocks and not at those which the
+// power cap leaves.  More warps (12 x 2 stages), smaller tiles and TMA boxes were slower.
 #include "sm100.cuh"
 
 namespace infllm2 {
