@@ -34,8 +34,8 @@
 // p_u scale_u >= 2^-25 R.
 //
 // Measured (one B200, sustained): 16 x 131072 8-bit, 1.11 GB, 186-205 us (5.4-6.0
-// TB/s; 32 heads), 175-181 us with 8 heads a group; 16 x 65536 bf16, 1.07 GB, 172-177 us; 64 bf16
-// sequences up to 8192, 0.27 GB, 57 us; one sequence of 1000 9.5 us.  A tile of the first costs its warp
+// TB/s; 32 heads), 175-181 us with 8 heads a group; 16 x 65536 bf16, 1.07 GB, 174 us; 64 bf16
+// sequences up to 8192, 0.27 GB, 58 us; one sequence of 1000 9.7 us.  A tile of the first costs its warp
 // 1800 cycles of products and softmax and 750 of copies and bookkeeping, with two warps
 // a scheduler.  That fits within the bandwidth at full clocks and not at those which the
 // power cap leaves.  More warps (12 x 2 stages), smaller tiles and TMA boxes were slower.
@@ -494,8 +494,10 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
         }
       }
   }
-  // probabilities: P in bf16 (relative error 2^-9 on a weight; the output itself is
-  // rounded to bf16 or its like), or w in f16; their sums stay in fp32 unrounded
+  // Probabilities as B fragments: w in f16, or P in bf16 twice, its rounded value
+  // and what that leaves (together 2^-16; one bf16 alone would add its 2^-8 to the output's
+  // own, for 1-2 % of the time: 57.0 against 58.2 us for 64 sequences up to 8192).  Their
+  // sums stay in fp32 unrounded.
   if constexpr (F8) {
     const float up = __uint_as_float(static_cast<uint32_t>(254 + 11 - st.e_r) << 23);
 #pragma unroll
@@ -506,7 +508,7 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
   for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
     for (int e = 0; e < 2; ++e) neg[nh][e] = st.m[nh][e] == -INFINITY ? 0.f : -st.m[nh][e];
-  uint32_t p[C::MT][NH][2];   // B fragments: 16 tokens x 8 heads
+  uint32_t p[C::MT][NH][2], rest[C::MT][NH][2];   // 16 tokens x 8 heads
 #pragma unroll
   for (int m = 0; m < C::MT; ++m)
 #pragma unroll
@@ -518,8 +520,14 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
         st.l[nh][e & 1] += w[e];
         if constexpr (F8) w[e] *= vs[2 * m + (e >> 1)];
       }
-      p[m][nh][0] = movmatrix(F8 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
-      p[m][nh][1] = movmatrix(F8 ? pack_f16(w[2], w[3]) : pack_bf16(w[2], w[3]));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = F8 ? pack_f16(w[2 * h], w[2 * h + 1]) : pack_bf16(w[2 * h], w[2 * h + 1]);
+        p[m][nh][h] = movmatrix(x);
+        if (!F8)
+          rest[m][nh][h] = movmatrix(pack_bf16(w[2 * h] - __uint_as_float(x << 16),
+                                               w[2 * h + 1] - __uint_as_float(x & 0xffff0000u)));
+      }
     }
   // O^T += V^T P^T
   const uint32_t vb = stage + kHalf;
@@ -562,6 +570,8 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
         ldsm_x4_t(f, vb + piece_at<C::CH, C::S, F8>(lane & 7, 2 * m + (i >> 1), 2 * j + (i & 1)));
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh) mma<false>(st.o[nh][j], f, p[m][nh][0], p[m][nh][1]);
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) mma<false>(st.o[nh][j], f, rest[m][nh][0], rest[m][nh][1]);
       }
     }
   }
