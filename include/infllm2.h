@@ -466,7 +466,10 @@ int infllm2_paged_read(const infllm2_paged_cache* c, void* K, void* V, const int
  * (device, on the current device; contents need no initialisation and carry
  * nothing between calls; one workspace must not serve two calls in flight at
  * once).  The result does not depend on scheduling.  Two launches, no host
- * synchronisation, graph-capturable; lengths may change between replays. */
+ * synchronisation, graph-capturable; lengths may change between replays.
+ * Lengths that change while a call is in flight (a caller's mistake in the
+ * order of its streams) leave its results undefined and may record
+ * INFLLM2_ERR_DEVICE_BOUNDS; no access leaves the buffers. */
 size_t infllm2_paged_workspace_bytes(const infllm2_paged_cache* c, int32_t h_q);
 int infllm2_paged_decode_attn(const infllm2_paged_cache* c, const void* q, int32_t h_q, const int32_t* seq_len,
                               void* out, int32_t out_dtype, float* lse, void* workspace, size_t workspace_bytes,

@@ -39,6 +39,7 @@
 // 1800 cycles of products and softmax and 750 of copies and bookkeeping, with two warps
 // a scheduler.  That fits within the bandwidth at full clocks and not at those which the
 // power cap leaves.  More warps (12 x 2 stages), smaller tiles and TMA boxes were slower.
+#include "paged_split.cuh"
 #include "sm100.cuh"
 
 namespace infllm2 {
@@ -48,7 +49,6 @@ namespace pattn {
 using dec::cp_async_commit;
 using dec::cp_async_wait_n;
 
-constexpr int kWarps = 8;
 constexpr int kStages = 3;
 constexpr int kUnit = 16;           // tokens; every page size is a multiple of it
 constexpr float kMargin = 4.f;      // the reference maximum is raised only past this many log2 units
@@ -124,7 +124,7 @@ struct Args {
   const __nv_bfloat16* q;
   void* out;
   float* lse;             // [batch, h_q] or null
-  int4* desc;             // workspace: what to join; by pair (first worker, CTAs, last worker or -1), by worker (pair, ...)
+  Join* desc;             // workspace: what to join, by pair or by worker
   float* part_o;          // workspace: [2 * workers][G][D]
   float* part_lse;        // workspace: [2 * workers][G]
   int32_t by_pair;        // at most as many pairs as workers
@@ -132,20 +132,17 @@ struct Args {
   float scale_log2;
 };
 
-// tiles of a sequence; a length outside [0, capacity] counts as 0 (recorded by CTA 0)
-template <int kTile>
-__device__ __forceinline__ int seq_tiles(const Args& a, int b) {
+// tokens of a sequence; a length outside [0, capacity] counts as 0 (recorded by CTA 0)
+__device__ __forceinline__ int seq_len(const Args& a, int b) {
   const int n = __ldg(a.len + b);
   const bool ok = n >= 0 && n <= static_cast<int64_t>(a.max_pages) << a.page_shift;
   if (!ok && blockIdx.x == 0) record_status(INFLLM2_ERR_DEVICE_BOUNDS);
-  return ok ? (n + kTile - 1) / kTile : 0;
+  return ok ? n : 0;
 }
+template <int kTile>
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 // a pair's share of the ranges
 __device__ __forceinline__ int pair_cost(int tiles) { return tiles > 0 ? tiles + 1 : 0; }
-
-__device__ __forceinline__ int64_t div_pos(int64_t x, int64_t y) {
-  return ((x | y) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
-}
 
 template <int D, bool F8>
 struct Cfg {
@@ -184,10 +181,19 @@ __device__ __forceinline__ uint32_t piece_at(int g, int x, int c) {
 // Walks the tiles of a warp's range.
 struct Walk {
   int b, g, n, t, te;   // sequence, kv head, its tiles, the next one, end of this piece
+  int len;              // the sequence's tokens
   int64_t left;         // cost of the range from the end of this piece on
   int tok_end;          // tokens of the piece end here
   const int32_t* row;   // the sequence's pages
 };
+
+// Takes sequence b.  Its length is read once, and lane 0's is the warp's: the warp's lanes walk together, and nothing
+// reads past a sequence's pages, whatever the length does meanwhile.
+template <int kTile>
+__device__ __forceinline__ void walk_seq(const Args& a, Walk& w) {
+  w.len = __shfl_sync(0xffffffffu, seq_len(a, w.b), 0);
+  w.n = tiles_of<kTile>(w.len);
+}
 
 // the piece of pair (b, g) from cost position y on; false when the range covers none of its tiles
 template <int kTile>
@@ -196,7 +202,7 @@ __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w, int y) {
   w.left -= take;
   w.t = max(y - 1, 0);
   w.te = y + take - 1;
-  w.tok_end = min(__ldg(a.len + w.b), w.te * kTile);
+  w.tok_end = min(w.len, w.te * kTile);
   w.row = a.table + static_cast<int64_t>(w.b) * a.max_pages;
   return w.t < w.te;
 }
@@ -210,7 +216,7 @@ __device__ __forceinline__ bool walk_pair(const Args& a, Walk& w) {
     w.g = 0;
     do {
       if (++w.b >= a.batch) return false;
-      w.n = seq_tiles<kTile>(a, w.b);
+      walk_seq<kTile>(a, w);
     } while (w.n == 0);
   }
   return walk_piece<kTile>(a, w, 0);   // an empty piece (the pair's start alone) ends its range
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
   const int per = (a.batch + 32 * kWarps - 1) / (32 * kWarps);
   const int b_lo = min(a.batch, static_cast<int>(threadIdx.x) * per), b_hi = min(a.batch, b_lo + per);
   int64_t incl = 0;
-  for (int b = b_lo; b < b_hi; ++b) incl += pair_cost(seq_tiles<C::kTile>(a, b));
+  for (int b = b_lo; b < b_hi; ++b) incl += pair_cost(tiles_of<C::kTile>(seq_len(a, b)));
   incl *= a.h_kv;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
   __syncthreads();
   // sequences with no keys: zeros and -inf
   for (int b = blockIdx.x * kWarps + warp; b < a.batch; b += a.ctas * kWarps) {
-    if (seq_tiles<C::kTile>(a, b) > 0) continue;
+    if (seq_len(a, b) > 0) continue;
     const int64_t row = static_cast<int64_t>(b) * a.h_kv * a.G;
     const int n = a.h_kv * a.G;
     for (int i = lane; i < n * D / 8; i += 32) {
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     if (a.lse)
       for (int i = lane; i < n; i += 32) a.lse[row + i] = -INFINITY;
     if (a.by_pair)
-      for (int i = lane; i < a.h_kv; i += 32) a.desc[static_cast<int64_t>(b) * a.h_kv + i] = make_int4(0, 0, -1, 0);
+      for (int i = lane; i < a.h_kv; i += 32) a.desc[static_cast<int64_t>(b) * a.h_kv + i] = Join{0, 0, -1, 0};
   }
 
   // this warp's range
@@ -743,7 +749,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
     int64_t cost = 1;
     prod.b = lo * per;
     for (; prod.b < a.batch; ++prod.b) {
-      prod.n = seq_tiles<C::kTile>(a, prod.b);
+      walk_seq<C::kTile>(a, prod);
       cost = pair_cost(prod.n);
       if (r < cost * a.h_kv) break;
       r -= cost * a.h_kv;
@@ -796,7 +802,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
         keep_piece<D, F8, NH>(st, reinterpret_cast<float*>(smem + warp * kStages * C::kStage), lane);
       else
         write_piece<D, F8, NH>(a, st, from0, pair, 2 * static_cast<int64_t>(wk), lane);
-      if (!keep && from0 && a.by_pair && lane == 0) a.desc[pair] = make_int4(0, 0, -1, 0);
+      if (!keep && from0 && a.by_pair && lane == 0) a.desc[pair] = Join{0, 0, -1, 0};
     }
     run = walk_next<C::kTile>(a, cons);
   }
@@ -854,21 +860,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attend_kernel(const __grid_con
       if (i % (D / 4) == 0 && (!out || a.lse)) (out ? a.lse : a.part_lse)[row0 + h] = lse;
     }
     if (warp == w0 && lane == 0) {   // its first warp describes a run
-      int4 joins = make_int4(a.by_pair ? wk : head.x, 0, -1, 0);
-      if (head.y && !tail.z) {
-        // the pair's end, its last worker, and whether that one goes on to another pair's tiles
-        const int64_t end = x1 + rest;
-        const int wl = static_cast<int>(div_pos(end - 1, share)), c1 = wl / kWarps;
-        const bool on = min(total, (wl + 1) * share) - end >= 2;
-        joins.y = c1 - static_cast<int>(blockIdx.x) + 1;
-        if (on && wl > max(wk, c1 * kWarps)) joins.z = wl;
-      }
+      Join joins{0, 0, -1, 0};
+      if (head.y && !tail.z) joins = describe_join(wk, head.x, x1, rest, share, total, a.ctas);
       if (!a.by_pair) a.desc[wk] = joins;
       else if (head.y) a.desc[head.x] = joins;
     }
-    if (!a.by_pair && lane == 0 && warp > w0 && warp <= w1) a.desc[wk] = make_int4(0, 0, -1, 0);
+    if (!a.by_pair && lane == 0 && warp > w0 && warp <= w1) a.desc[wk] = Join{0, 0, -1, 0};
   }
-  if (!a.by_pair && last.x < 0 && lane == 0) a.desc[wk] = make_int4(0, 0, -1, 0);
+  if (!a.by_pair && last.x < 0 && lane == 0) a.desc[wk] = Join{0, 0, -1, 0};
 }
 
 // Joins the partials of the (sequence, kv head) pairs that several ranges share:
@@ -889,15 +888,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   const int at = row / a.G, h = row - at * a.G;
   dec::griddep_wait();
   if (row >= rows) return;
-  const int4 d = a.desc[at];
-  if (d.y == 0) return;                 // written by its warps
-  const int np = d.y + (d.z >= 0 ? 1 : 0);
-  const int wk = a.by_pair ? d.x : at, pair = a.by_pair ? at : d.x;
-  // the second slot of wk, the first slots of the next CTAs' first workers, and that of worker d.z
-  auto slot = [&](int i) {
-    const int w = i == 0 ? wk : i < d.y ? (wk / kWarps + i) * kWarps : d.z;
-    return static_cast<int64_t>(2 * w + (i == 0 ? 1 : 0)) * a.G + h;
-  };
+  const Join d = a.desc[at];
+  if (d.ctas == 0) return;              // written by its warps
+  if (!join_in_bounds(d, a.batch * a.h_kv, a.ctas)) {   // (lengths that changed under the call)
+    if (threadIdx.x % 32 == 0) record_status(INFLLM2_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  const int np = join_pieces(d), pair = d.pair;
+  auto slot = [&](int i) { return static_cast<int64_t>(join_slot(d, i)) * a.G + h; };
   const int c = threadIdx.x % LPR, r = (threadIdx.x % (32 * WPR)) / LPR;
   // this thread's pieces with a running maximum, eight loads in flight
   float m = -INFINITY, l = 0.f;
@@ -977,7 +975,7 @@ static Plan plan(int G, int d, int ctas) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = static_cast<size_t>(2) * ctas * kWarps;
   Plan p;
-  p.off_lse = up(slots / 2 * sizeof(int4));   // pairs (at most workers), or workers
+  p.off_lse = up(slots / 2 * sizeof(Join));   // pairs (at most workers), or workers
   p.off_o = p.off_lse + up(slots * G * 4);
   p.bytes = p.off_o + up(slots * G * d * 4);
   return p;
@@ -1026,7 +1024,7 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
 cudaError_t launch_paged_attn(pattn::Args a, int d, bool f8, void* workspace, cudaStream_t st) {
   const pattn::Plan p = pattn::plan(a.G, d, a.ctas);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.desc = reinterpret_cast<int4*>(ws);
+  a.desc = reinterpret_cast<pattn::Join*>(ws);
   a.by_pair = static_cast<int64_t>(a.batch) * a.h_kv <= static_cast<int64_t>(a.ctas) * pattn::kWarps;
   a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
   a.part_o = reinterpret_cast<float*>(ws + p.off_o);
