@@ -29,9 +29,10 @@
 // 8 bits.  K and V go from e4m3 to f16 exactly.  q is scaled to f16 by a power
 // of two a head (its 8 significant bits are kept down to 2^-29 of the head's
 // largest element, and 2^-39 of it absolutely).  A value's scale multiplies its
-// probability: w_u = p_u * scale_u / R * 2^11 in f16, with R a power of two no
-// less than any scale seen and p_u <= 2^kMargin, so w keeps 11 bits where
-// p_u scale_u >= 2^-25 R.
+// probability: w_u = p_u scale_u c in f16, with c a power of two a head that brings the
+// head's largest p_u scale_u so far to 2^11 (2^(11 + kMargin) before c is lowered).
+// What counts is p scale and not the scale alone: a large row of no weight
+// leaves c as it is, and w keeps 11 bits down to 2^-25 of the head's largest.
 //
 // Measured (one B200, sustained): 16 x 131072 8-bit, 1.11 GB, 186-205 us (5.4-6.0
 // TB/s; 32 heads), 175-181 us with 8 heads a group; 16 x 65536 bf16, 1.07 GB, 174 us; 64 bf16
@@ -51,7 +52,8 @@ using dec::cp_async_wait_n;
 
 constexpr int kStages = 3;
 constexpr int kUnit = 16;           // tokens; every page size is a multiple of it
-constexpr float kMargin = 4.f;      // the reference maximum is raised only past this many log2 units
+constexpr float kMargin = 4.f;      // a reference is raised only past this many log2 units
+constexpr float kTop = 11.f;        // 8 bits: log2 of the weight that the reference stands for
 constexpr int kHalf = 4096;         // bytes of K, and of V, in a stage
 
 // The products, the transposed loads and movmatrix are plain (not volatile) asm, so
@@ -103,6 +105,14 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+// (subnormal numbers included)
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2_of(float e) { return __int_as_float((static_cast<int>(e) + 127) << 23); }
+__device__ __forceinline__ float exponent_of(float p) { return static_cast<float>((__float_as_int(p) >> 23) - 127); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -374,7 +384,8 @@ struct State {
   float o[NH][D / 16][4];   // O^T tiles: rows gid and gid + 8
   float m[NH][2];           // reference maximum, log2 units (the same in all lanes of a head)
   float l[NH][2];           // this lane's share of the sum
-  int e_r;                  // F8: R = 2^(e_r - 127)
+  float c[NH][2];           // F8: the weights' factor, 2^(kTop + m - (log2 of the reference p scale))
+  float lim[NH][2];         // F8: log2 of the weight, without c, past which the reference is raised
 };
 
 template <int D, bool F8, int NH>
@@ -385,8 +396,9 @@ __device__ __forceinline__ void state_clear(State<D, F8, NH>& s) {
     for (int i = 0; i < D / 16; ++i) s.o[nh][i][0] = s.o[nh][i][1] = s.o[nh][i][2] = s.o[nh][i][3] = 0.f;
     s.m[nh][0] = s.m[nh][1] = -INFINITY;
     s.l[nh][0] = s.l[nh][1] = 0.f;
+    s.c[nh][0] = s.c[nh][1] = 1.f;
+    s.lim[nh][0] = s.lim[nh][1] = -INFINITY;
   }
-  s.e_r = 16;
 }
 
 template <int D, bool F8, int NH>
@@ -454,8 +466,15 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
         for (int e = 0; e < 4; ++e)
           if (C::S * gid + 2 * m + (e >> 1) >= nv) z[m][nh][e] = -INFINITY;
   }
-  // raise the reference maximum (and R) where a score (a scale) passes it
-  float top[NH][2];
+  // Raise a reference where a score (F8: or a score with its value's scale) passes it.  The second is
+  // bounded by the lane's largest score and largest scale, which differ little over a few consecutive tokens.
+  float top[NH][2], vtop = -INFINITY;
+  if constexpr (F8) {
+    vtop = 0.f;
+#pragma unroll
+    for (int i = 0; i < C::S; ++i) vtop = fmaxf(vtop, fabsf(vs[i]));
+    vtop = lg2(vtop);
+  }
   bool past = false;
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh)
@@ -466,20 +485,13 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
       for (int m = 0; m < C::MT; ++m) t = fmaxf(t, fmaxf(z[m][nh][e], z[m][nh][2 + e]));
       top[nh][e] = t * q.s[nh][e];
       past = past || top[nh][e] > st.m[nh][e] + kMargin;
+      if constexpr (F8) past = past || top[nh][e] + vtop > st.lim[nh][e];
     }
-  float vtop = 0.f;
-  if constexpr (F8) {
-#pragma unroll
-    for (int i = 0; i < C::S; ++i) vtop = fmaxf(vtop, fabsf(vs[i]));
-    past = past || vtop > __uint_as_float(static_cast<uint32_t>(st.e_r) << 23);
-  }
   if (__any_sync(0xffffffffu, past)) {
-    float back = 1.f;   // F8: R before / R now
+    float lv[F8 ? C::S : 1];
     if constexpr (F8) {
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(vtop));
-      const int e = min(max(static_cast<int>((bits + 0x7fffffu) >> 23), st.e_r), 250);
-      back = e - st.e_r > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + st.e_r - e) << 23);
-      st.e_r = e;
+#pragma unroll
+      for (int i = 0; i < C::S; ++i) lv[i] = lg2(fabsf(vs[i]));
     }
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
@@ -489,14 +501,32 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-        const float m = fmaxf(st.m[nh][e], t);
+        // (F8: whole log2 units, so that factors are powers of two)
+        const float m = fmaxf(st.m[nh][e], F8 ? ceilf(t) : t);
         const float f = st.m[nh][e] == m ? 1.f : ex2(st.m[nh][e] - m);
+        float back = f;
+        if constexpr (F8) {
+          float y = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < C::MT; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) y = fmaxf(y, fmaf(z[k][nh][2 * h + e], q.s[nh][e], lv[2 * k + h]));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          y = fmaxf(st.lim[nh][e] - kMargin, ceilf(y));
+          // c, 1 / c and 1 / (l c) stay normal numbers (m = -inf, where nothing has a weight yet: any c)
+          const float was = exponent_of(st.c[nh][e]), now = fminf(fmaxf(kTop + m - y, -118.f), 104.f);
+          back = ex2((st.m[nh][e] == m ? 0.f : st.m[nh][e] - m) + (now - was));
+          st.c[nh][e] = pow2_of(now);
+          st.lim[nh][e] = m + (kTop + kMargin - now);
+        }
         st.m[nh][e] = m;
         st.l[nh][e] *= f;
 #pragma unroll
         for (int i = 0; i < C::DT; ++i) {
-          st.o[nh][i][e] *= f * back;
-          st.o[nh][i][2 + e] *= f * back;
+          st.o[nh][i][e] *= back;
+          st.o[nh][i][2 + e] *= back;
         }
       }
   }
@@ -504,11 +534,6 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
   // and what that leaves (together 2^-16; one bf16 alone would add its 2^-8 to the output's
   // own, for 1-2 % of the time: 57.0 against 58.2 us for 64 sequences up to 8192).  Their
   // sums stay in fp32 unrounded.
-  if constexpr (F8) {
-    const float up = __uint_as_float(static_cast<uint32_t>(254 + 11 - st.e_r) << 23);
-#pragma unroll
-    for (int i = 0; i < C::S; ++i) vs[i] *= up;
-  }
   float neg[NH][2];
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh)
@@ -524,7 +549,7 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
       for (int e = 0; e < 4; ++e) {
         w[e] = ex2(fmaf(z[m][nh][e], q.s[nh][e & 1], neg[nh][e & 1]));
         st.l[nh][e & 1] += w[e];
-        if constexpr (F8) w[e] *= vs[2 * m + (e >> 1)];
+        if constexpr (F8) w[e] = w[e] * vs[2 * m + (e >> 1)] * st.c[nh][e & 1];
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -608,8 +633,7 @@ __device__ __forceinline__ void row_stats(const State<D, F8, NH>& st, int nh, in
   l += __shfl_xor_sync(0xffffffffu, l, 4);
   l += __shfl_xor_sync(0xffffffffu, l, 8);
   l += __shfl_xor_sync(0xffffffffu, l, 16);
-  inv = l == 0.f ? 0.f : 1.f / l;
-  if (F8) inv *= __uint_as_float(static_cast<uint32_t>(st.e_r - 11) << 23);
+  inv = l == 0.f ? 0.f : 1.f / (F8 ? l * st.c[nh][e] : l);
   lse = l == 0.f ? -INFINITY : st.m[nh][e] + log2f(l);
 }
 
