@@ -459,11 +459,13 @@ int infllm2_paged_read(const infllm2_paged_cache* c, void* K, void* V, const int
  *   q    bf16 [batch, h_q, d];  out [batch, h_q, d] bf16 or fp32 (out_dtype)
  *   lse  fp32 [batch, h_q], or NULL
  * A sequence of length 0, or whose every score is -infinity, gives zeros and
- * -infinity.  Slots at or past seq_len[b] are not read.  A length outside
- * [0, max_pages * page_size] is recorded as INFLLM2_ERR_DEVICE_BOUNDS and
- * counts as 0; rows of a page out of range count as zeros.
+ * -infinity.  An infinite element of a bf16 V row gives that infinity, in its
+ * own column, wherever the row's weight is above 0 in fp32.  Slots at or past
+ * seq_len[b] are not read.  A length outside [0, max_pages * page_size] is
+ * recorded as INFLLM2_ERR_DEVICE_BOUNDS and counts as 0; rows of a page out of
+ * range count as zeros.
  * Scores, softmax statistics and sums are fp32.  For the product with V a weight
- * is held in two bf16 numbers (2^-16 of it), or, times the value's scale, in one f16
+ * is held in two bf16 numbers (2^-15 of it), or, times the value's scale, in one f16
  * number (8-bit pages: 2^-11 of it, with fewer bits below 2^-25 of the largest weight
  * times scale of its head), whatever the output's type.
  * Of p, scale is used.  workspace: at least infllm2_paged_workspace_bytes bytes

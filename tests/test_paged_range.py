@@ -1,10 +1,11 @@
 """The paged decode attention over keys, values and queries of very different sizes, against 64 bits.
 
 Tolerances are those of the ordinary rows: z's fp32 sum of d products, (d + 4) 2^-22 of the largest sum of their
-magnitudes, so twice that times ln 2 on a weight; 2^-11 a weight of 8-bit pages (2^-16 in two bf16 parts); the fp32 sums,
-2^-18 + 2^-22 n / 32; all relative to sum p |v|, and the output's half step.  A weight so small that its part in 16 bits
-has fewer than 11 bits is off by 2^-36 of the largest p scale of its head at most, times 448 for a value; n of them:
-n 2^-27 max(p scale) is added for 8-bit pages.
+magnitudes, so twice that times ln 2 on a weight; 2^-11 a weight of 8-bit pages; 2^-15 one in two bf16 parts (what its
+upper half leaves is below 2^-7, rounded to 2^-8 of that); the fp32 sums, 2^-18 + 2^-22 n / 32; all relative to
+sum p |v|, and the output's half step.  A weight so small that its part in 16 bits has fewer than 11 bits is off by 2^-36
+of the largest p scale of its head at most, times 448 for a value; n of them: n 2^-27 max(p scale) is added for 8-bit
+pages.
 
 A softmax in 32 bits has no weights below 2^-126, fp32's smallest normal number.  A weight is held relative to the largest
 of its part (up to 2 of them: the reference is a whole number of log2 units at most 1 above), and a part relative to the
@@ -61,7 +62,7 @@ def _check(K, V, q, e4m3):
     zmag = torch.einsum("hd,hnd->hn", x.abs(), k.abs()).amax(-1) * scale / math.log(2)
     dz = (d + 4) * 2.0 ** -22 * zmag
     sums = 2.0 ** -22 * n / 32 + 2.0 ** -18
-    tol = mag * ((2.0 ** -11 if e4m3 else 2.0 ** -16) + sums + 2 * math.log(2) * dz[:, None])
+    tol = mag * ((2.0 ** -11 if e4m3 else 2.0 ** -15) + sums + 2 * math.log(2) * dz[:, None])
     tol += ref.abs() * 2.0 ** -24 + n * 2.0 ** -27 * (p * s).amax(-1)[:, None]
     tol += torch.einsum("hn,hnd->hd", torch.where(p < 2.0 ** -125 * n * p.amax(-1, keepdim=True), p, 0.0), v.abs())
     out, got = _attend(cache, q, n)
@@ -120,3 +121,31 @@ def test_values_of_one_far_size(size):
     V *= 2.0 ** size
     q = torch.randn(1, 8, 128, device="cuda", generator=torch.Generator("cuda").manual_seed(4))
     _check(K.bfloat16(), V.bfloat16(), q.bfloat16(), True)
+
+
+@pytest.mark.parametrize("h_q,h_kv,d,n", [(16, 1, 128, 1), (16, 1, 128, 3000), (8, 2, 64, 100), (1, 1, 128, 33)])
+@pytest.mark.parametrize("same", [True, False])
+def test_infinite_values(h_q, h_kv, d, n, same):
+    # bf16 pages: a weight above 0 times an infinity is that infinity, in its column alone, whether the weight has
+    # 8 bits (equal scores: exactly 1) or more; infinities of both signs are NaN
+    K, V = _rows(n, h_kv, d, 15)
+    q = torch.randn(1, h_q, d, device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    if same:
+        K[:] = 0
+    V[n // 2, :, 3], V[n - 1, :, 5], V[n // 3, :, 17], V[0, :, 40] = math.inf, -math.inf, math.inf, -math.inf
+    V[0, :, 41] = math.inf
+    V[n - 1, :, 41] = -math.inf
+    K, V, q = K.bfloat16(), V.bfloat16(), q.bfloat16()
+    cache, k, v, _ = _cache(K, V, False)
+    g = h_q // h_kv
+    k, v = (x.repeat_interleave(g, 0) for x in (k, v))
+    p = (torch.einsum("hd,hnd->hn", q[0].double(), k) / math.sqrt(d)).softmax(-1)
+    ref = (p[..., None] * v).sum(1)
+    assert ref[:, 3].eq(math.inf).all() and (n == 1 or ref[:, 41].isnan().all())
+    for dtype in (torch.float32, torch.bfloat16):
+        out, lse = _attend(cache, q, n, dtype)
+        odd = ~ref.isfinite()
+        assert torch.equal(out.isnan(), ref.isnan())
+        assert torch.equal(out[odd & ~ref.isnan()], ref[odd & ~ref.isnan()])
+        assert lse.isfinite().all()
+        assert ((out - ref).abs()[~odd] <= 2.0 ** -7 * v[v.isfinite()].abs().max()).all()

@@ -530,10 +530,12 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
         }
       }
   }
-  // Probabilities as B fragments: w in f16, or P in bf16 twice, its rounded value
-  // and what that leaves (together 2^-16; one bf16 alone would add its 2^-8 to the output's
+  // Probabilities as B fragments: w in f16, or P in bf16 twice, its upper half and
+  // what that leaves (together 2^-15; one bf16 alone would add its 2^-8 to the output's
   // own, for 1-2 % of the time: 57.0 against 58.2 us for 64 sequences up to 8192).  Their
-  // sums stay in fp32 unrounded.
+  // sums stay in fp32 unrounded.  Both parts of a P above 0 are above 0 (the upper half is cut off, not
+  // rounded, and 2^-22 P added to the rest), so an infinite value gives that infinity twice and never
+  // inf - inf or 0 inf.
   float neg[NH][2];
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh)
@@ -553,11 +555,14 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t x = F8 ? pack_f16(w[2 * h], w[2 * h + 1]) : pack_bf16(w[2 * h], w[2 * h + 1]);
+        const uint32_t x = F8 ? pack_f16(w[2 * h], w[2 * h + 1])
+                              : __byte_perm(__float_as_uint(w[2 * h]), __float_as_uint(w[2 * h + 1]), 0x7632);
         p[m][nh][h] = movmatrix(x);
-        if (!F8)
-          rest[m][nh][h] = movmatrix(pack_bf16(w[2 * h] - __uint_as_float(x << 16),
-                                               w[2 * h + 1] - __uint_as_float(x & 0xffff0000u)));
+        if (!F8) {
+          constexpr float kUp = 1.f + 1.f / (1 << 22);
+          rest[m][nh][h] = movmatrix(pack_bf16(fmaf(w[2 * h], kUp, -__uint_as_float(x << 16)),
+                                               fmaf(w[2 * h + 1], kUp, -__uint_as_float(x & 0xffff0000u))));
+        }
       }
     }
   // O^T += V^T P^T
