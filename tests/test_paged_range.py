@@ -149,3 +149,16 @@ def test_infinite_values(h_q, h_kv, d, n, same):
         assert torch.equal(out[odd & ~ref.isnan()], ref[odd & ~ref.isnan()])
         assert lse.isfinite().all()
         assert ((out - ref).abs()[~odd] <= 2.0 ** -7 * v[v.isfinite()].abs().max()).all()
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("h_q,d", [(16, 128), (8, 128), (16, 64), (2, 64)])
+@pytest.mark.parametrize("q_size,k_size", [(-110, 110), (-98, 100), (-112, 118), (-60, 60), (100, -98), (112, -108)])
+def test_scores_of_far_queries_and_keys(q_size, k_size, h_q, d, e4m3):
+    # ordinary scores, of factors that are not
+    n = 300
+    K, V = _rows(n, 1, d, 17)
+    q = torch.randn(1, h_q, d, device="cuda", generator=torch.Generator("cuda").manual_seed(6))
+    K, q = K * 2.0 ** k_size, q * 2.0 ** q_size
+    K[::7] *= 2.0 ** (-40 if k_size > 0 else 0)      # large and ordinary rows side by side
+    _check(K.bfloat16(), V.bfloat16(), q.bfloat16(), e4m3)

@@ -105,6 +105,14 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+// two fp32 products in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 // (subnormal numbers included)
 __device__ __forceinline__ float lg2(float x) {
   float y;
@@ -450,12 +458,22 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
       vs[4 * i] = __uint_as_float(v.x); vs[4 * i + 1] = __uint_as_float(v.y);
       vs[4 * i + 2] = __uint_as_float(v.z); vs[4 * i + 3] = __uint_as_float(v.w);
     }
+    // Scores in log2 units.  q's factor comes first: a product is below 2^31 (448 d 2^15), and times a large scale
+    // it would overflow before a small factor brings it down.  Two factors a score cost 8 instructions a tile and eight
+    // heads in packed form; the other way, smaller key scales where one is past 2^96, is a branch in every tile (16 x
+    // 131072 212.4 us packed, 214.1 with the branch).
 #pragma unroll
     for (int m = 0; m < C::MT; ++m)
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[m][nh][e] *= ks[2 * m + (e >> 1)];
+        for (int h = 0; h < 2; ++h) {
+          const float x = ks[2 * m + h];
+          const float2 y = mul2(mul2(make_float2(z[m][nh][2 * h], z[m][nh][2 * h + 1]),
+                                     make_float2(q.s[nh][0], q.s[nh][1])), make_float2(x, x));
+          z[m][nh][2 * h] = y.x;
+          z[m][nh][2 * h + 1] = y.y;
+        }
   }
   if (nv < C::kTile) {
 #pragma unroll
@@ -483,7 +501,7 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
       float t = -INFINITY;
 #pragma unroll
       for (int m = 0; m < C::MT; ++m) t = fmaxf(t, fmaxf(z[m][nh][e], z[m][nh][2 + e]));
-      top[nh][e] = t * q.s[nh][e];
+      top[nh][e] = F8 ? t : t * q.s[nh][e];
       past = past || top[nh][e] > st.m[nh][e] + kMargin;
       if constexpr (F8) past = past || top[nh][e] + vtop > st.lim[nh][e];
     }
@@ -510,7 +528,7 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
 #pragma unroll
           for (int k = 0; k < C::MT; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) y = fmaxf(y, fmaf(z[k][nh][2 * h + e], q.s[nh][e], lv[2 * k + h]));
+            for (int h = 0; h < 2; ++h) y = fmaxf(y, z[k][nh][2 * h + e] + lv[2 * k + h]);
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
@@ -549,9 +567,18 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
       float w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        w[e] = ex2(fmaf(z[m][nh][e], q.s[nh][e & 1], neg[nh][e & 1]));
+        w[e] = ex2(F8 ? z[m][nh][e] + neg[nh][e & 1] : fmaf(z[m][nh][e], q.s[nh][e & 1], neg[nh][e & 1]));
         st.l[nh][e & 1] += w[e];
-        if constexpr (F8) w[e] = w[e] * vs[2 * m + (e >> 1)] * st.c[nh][e & 1];
+      }
+      if constexpr (F8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = vs[2 * m + h];
+          const float2 y = mul2(mul2(make_float2(w[2 * h], w[2 * h + 1]), make_float2(x, x)),
+                                make_float2(st.c[nh][0], st.c[nh][1]));
+          w[2 * h] = y.x;
+          w[2 * h + 1] = y.y;
+        }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
