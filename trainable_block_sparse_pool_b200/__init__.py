@@ -382,7 +382,8 @@ def infllm2_decode_step(st: DecodeState, q: torch.Tensor, k_new: torch.Tensor, v
 # ------------------------------------------------------------------ rotary positions, paged cache
 # (These calls check every tensor they are given.  The checks are plain attribute reads: on a short call they, the
 # argument conversion and the launch take about 2 us each, more than the kernel.)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # noqa: SLF001  (current_stream(), unwrapped)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",  # noqa: SLF001  (current_stream(), unwrapped)
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _expect(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
