@@ -467,9 +467,11 @@ int infllm2_paged_read(const infllm2_paged_cache* c, void* K, void* V, const int
  * Scores, softmax statistics and sums are fp32.  For the product with V a weight
  * is held in two bf16 numbers (2^-15 of it), or, times the value's scale, in one f16
  * number (8-bit pages: 2^-11 of it, with fewer bits below 2^-25 of the largest weight
- * times scale of its head), whatever the output's type.  8-bit pages: the query's
- * product with a row's 8-bit values, times the softmax scale, has to stay below 2^128
- * (it does for scores up to 512 log2 units at the smallest scale that infllm2_paged_write gives).
+ * times scale of its head), whatever the output's type.  8-bit pages: a query
+ * element below 2^-29 of its head's largest loses bits and is 0 below 2^-39, and
+ * the query's product with a row's 8-bit values, times the softmax scale, has to
+ * stay below 2^128 (it does for scores up to 512 log2 units at the smallest scale
+ * that infllm2_paged_write gives).
  * Of p, scale is used.  workspace: at least infllm2_paged_workspace_bytes bytes
  * (device, on the current device; contents need no initialisation and carry
  * nothing between calls; one workspace must not serve two calls in flight at

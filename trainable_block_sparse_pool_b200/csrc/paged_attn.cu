@@ -175,13 +175,9 @@ struct Cfg {
   static constexpr int DT = D / 16;                   // 16-column tiles of O^T
 };
 
-// Row R = g + 8h (g < 8, h < 2) of the tile's S^T tile m is its token S g + 2 m + h: the
+// Row g + 8h (g < 8, h < 2) of the tile's S^T tile m is its token S g + 2 m + h: the
 // order is free (probabilities and values use the same one), and this one gives
 // lane group g the S consecutive tokens from S g on, so its scales are vectors.
-template <int S>
-__device__ __forceinline__ int row_token(int m, int R) {
-  return S * (R & 7) + 2 * m + (R >> 3);
-}
 
 // Shared-memory byte of 16-byte piece c of the tile's token S g + x.  Rows of 128
 // bytes or more have lines of their own, the piece XORed with a number made of
