@@ -451,8 +451,9 @@ int infllm2_paged_read(const infllm2_paged_cache* c, void* K, void* V, const int
                        void* stream);
 
 /* Attention of one new token a sequence over its whole paged cache, the dense
- * side of the dense/sparse switch at decode (a sequence past dense_threshold
- * goes to infllm2_decode_step).  For query head h of group g and n = seq_len[b]
+ * side of the dense/sparse switch at decode (past dense_threshold the model's
+ * switch means infllm2_decode_step; this call takes any length that the table
+ * holds).  For query head h of group g and n = seq_len[b]
  * (device, int32 [batch]; the new token's own row already written):
  *   out[b,h] = sum_{u<n} softmax_u(scale * q[b,h] . K[u,g]) V[u,g]
  *   lse[b,h] = log2 sum_{u<n} 2^(scale * log2(e) * q[b,h] . K[u,g])

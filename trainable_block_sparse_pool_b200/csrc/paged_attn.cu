@@ -34,9 +34,9 @@
 // What counts is p scale and not the scale alone: a large row of no weight
 // leaves c as it is, and w keeps 11 bits down to 2^-25 of the head's largest.
 //
-// Measured (one B200, sustained): 16 x 131072 8-bit, 1.11 GB, 186-205 us (5.4-6.0
-// TB/s; 32 heads), 175-181 us with 8 heads a group; 16 x 65536 bf16, 1.07 GB, 174 us; 64 bf16
-// sequences up to 8192, 0.27 GB, 58 us; one sequence of 1000 9.7 us.  A tile of the first costs its warp
+// Measured (one B200, sustained): 16 x 131072 8-bit, 1.11 GB, 193-215 us (5.1-5.7
+// TB/s; 32 heads), 178-181 us with 8 heads a group; 16 x 65536 bf16, 1.07 GB, 175-179 us; 64 bf16
+// sequences up to 8192, 0.27 GB, 57 us; one sequence of 1000 10 us.  A tile of the first costs its warp
 // 1800 cycles of products and softmax and 750 of copies and bookkeeping, with two warps
 // a scheduler.  That fits within the bandwidth at full clocks and not at those which the
 // power cap leaves.  More warps (12 x 2 stages), smaller tiles and TMA boxes were slower.
@@ -546,8 +546,9 @@ __device__ __forceinline__ void attend_tile(State<D, F8, NH>& st, const Query<D,
   }
   // Probabilities as B fragments: w in f16, or P in bf16 twice, its upper half and
   // what that leaves (together 2^-15; one bf16 alone would add its 2^-8 to the output's
-  // own, for 1-2 % of the time: 57.0 against 58.2 us for 64 sequences up to 8192).  Their
-  // sums stay in fp32 unrounded.  Both parts of a P above 0 are above 0 (the upper half is cut off, not
+  // own, for 1-2 % of the time: 57.0 against 58.2 us for 64 sequences up to 8192).  (A second f16
+  // part of w changes the third digit of a bf16 output's error and takes 235 us for 207 at 16 x
+  // 131072.)  The sums of both stay in fp32 unrounded.  Both parts of a P above 0 are above 0 (the upper half is cut off, not
   // rounded, and 2^-22 P added to the rest), so an infinite value gives that infinity twice and never
   // inf - inf or 0 inf.
   float neg[NH][2];

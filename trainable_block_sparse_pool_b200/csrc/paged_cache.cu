@@ -11,7 +11,7 @@
 // HBM-bound.  A row belongs to d / 16 lanes, each with two 16-byte pieces of it
 // (the row's K and V together: four independent loads a thread, on a write issued
 // before the search for the row's sequence and page).  131072 8-bit rows of two kv
-// heads are written in 34 us (floor 31.0 at the measured copy rate), 65521 read
+// heads are written in 34-37 us (floor 31.0 at the measured copy rate), 65521 read
 // in 18.6 us (15.5), of which the launch is about 2.  Two rows a thread, for more
 // loads behind one chain of lookups, were slower (37.0 and 19.1 us).
 #include "sm100.cuh"

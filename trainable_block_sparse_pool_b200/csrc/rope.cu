@@ -15,8 +15,8 @@
 // eight pairs of a token (16-byte vectors that neighbouring threads hold side by
 // side) and walks several heads of it with the same sines and cosines in
 // registers, its loads of all heads in flight before the angles are computed.
-// 32768 tokens of 32 + 2 heads in bf16 take 90-96 us (571 MB, 91-97 % of the
-// measured copy rate), an fp32 interleaved backward of 9973 tokens 55.7 us (95 %).
+// 32768 tokens of 32 + 2 heads in bf16 take 90-100 us (571 MB, 87-97 % of the
+// measured copy rate), an fp32 interleaved backward of 9973 tokens 55-57 us (93-96 %).
 #include "sm100.cuh"
 
 namespace infllm2 {
